@@ -447,6 +447,62 @@ lcsa_status lcsa_csa_sparse_attn_fp8(const lcsa_attn_args* a, const lcsa_fp8_ent
 lcsa_status lcsa_hca_dense_attn_fp8(const lcsa_attn_args* a, const lcsa_fp8_entries* e, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * FP4 entry cache ([p4] "三、FP4量化": E2M1 with block scales; "KV Cache优化细节":
+ * the rotary dims stay BF16).  The pages hold the compressed KV entries in FP8
+ * and only the indexer's keys in FP4; this is the same entry cache with an
+ * MXFP4 body, for contexts whose FP8 entries do not fit.  Per entry row
+ * x[0..D):
+ *   - body x[0..D-R): blocks of 32 values, codes and scale bytes by the rule of
+ *     lcsa_quantize_mxfp4 (E2M1, ties to even, saturating at 6, X + 127; a
+ *     block holding Inf or NaN: byte 255 and zero codes, read back as NaN);
+ *   - rotary dims x[D-R..D): BF16 (round to nearest even).
+ * Every value that the cache stands for is a BF16 number, so reading it back
+ * rounds nothing.  Bytes per entry at D=512, R=64: 224 + 16 + 128 = 368 against
+ * 1024 (BF16) and 577 (FP8).
+ *
+ *   codes  [B,cache_rows,(D-R)/2] uint8, the even element in the low nibble
+ *   scales [B,cache_rows,S] uint8, S = lcsa_fp4_scale_bytes(D, R): (D-R)/32
+ *          scale bytes, padded with zeros to a multiple of 16
+ *   rope   [B,cache_rows,R] BF16
+ * Constraints: D-R a positive multiple of 32, R >= 0 a multiple of 8, all
+ * pointers 16-byte aligned (rope may be NULL when R = 0); otherwise
+ * LCSA_ERR_INVALID_ARG.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  void* rope;
+} lcsa_fp4_entries;
+
+size_t lcsa_fp4_scale_bytes(int D, int R);
+
+/* Writes rows x [B,n,D] (dtype) into rows row0 .. row0+n-1 of every sequence of
+ * the cache (a decode step appends, a prefill writes from row 0); nothing else
+ * is touched.  Codes and scales are a pure function of x.  row0 < 0 or
+ * row0 + n > cache_rows: LCSA_ERR_INVALID_ARG. */
+lcsa_status lcsa_quantize_entries_fp4(const void* x, int B, int64_t n, int D, int R, lcsa_dtype dtype,
+                                      const lcsa_fp4_entries* cache, int64_t cache_rows, int64_t row0, void* stream);
+
+/* Reads rows back: out [B,n,D] out_dtype, row r of sequence b = entry idx[b,r]
+ * (idx [B,n] int32; NULL: entry r, n <= cache_rows).  Index -1 gives a zero row;
+ * any other index outside [0, cache_rows) gives a zero row and
+ * LCSA_DEV_BAD_INDEX. */
+lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, int64_t cache_rows, int D, int R,
+                                        const int32_t* idx, int64_t n, void* out, lcsa_dtype out_dtype, void* stream);
+
+/* Core attention (as lcsa_csa_sparse_attn / lcsa_hca_dense_attn) over entries
+ * held in the FP4 cache `e` with cache_rows = a->Nc, instead of a->ckv (not
+ * read; may be NULL).  Every other argument and result is that of the BF16
+ * calls on the entries read back; R must meet the cache's constraints.  Rows
+ * that a query does not attend to are not read: what they hold (Inf, NaN) does
+ * not reach its output.  The workspace is lcsa_attn_fp4_workspace bytes. */
+size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse);
+lcsa_status lcsa_csa_sparse_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+lcsa_status lcsa_hca_dense_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

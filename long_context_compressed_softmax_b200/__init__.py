@@ -35,6 +35,8 @@ EXPORTED = [
     "lcsa_grouped_out_proj_workspace", "lcsa_grouped_out_proj",
     "lcsa_attn_workspace", "lcsa_csa_sparse_attn", "lcsa_hca_dense_attn", "lcsa_attn_uses_tensor_cores",
     "lcsa_quantize_entries_fp8", "lcsa_csa_sparse_attn_fp8", "lcsa_hca_dense_attn_fp8",
+    "lcsa_fp4_scale_bytes", "lcsa_quantize_entries_fp4", "lcsa_dequantize_entries_fp4",
+    "lcsa_attn_fp4_workspace", "lcsa_csa_sparse_attn_fp4", "lcsa_hca_dense_attn_fp4",
     "lcsa_set_wait_limit_ns", "lcsa_test_withhold_stage", "lcsa_set_attn_gather", "lcsa_set_fp4_mma",
 ]
 
@@ -88,6 +90,10 @@ class Fp8Entries(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rope", ctypes.c_void_p)]
 
 
+class Fp4Entries(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rope", ctypes.c_void_p)]
+
+
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _sig = {
     "lcsa_version": (ctypes.c_char_p, []),
@@ -114,6 +120,12 @@ _sig = {
     "lcsa_hca_dense_attn": (_i, [ctypes.POINTER(AttnArgs), _vp, _sz, _vp]),
     "lcsa_attn_uses_tensor_cores": (_i, [ctypes.POINTER(AttnArgs)]),
     "lcsa_quantize_entries_fp8": (_i, [_vp, _i64, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "lcsa_fp4_scale_bytes": (_sz, [_i, _i]),
+    "lcsa_quantize_entries_fp4": (_i, [_vp, _i, _i64, _i, _i, _i, ctypes.POINTER(Fp4Entries), _i64, _i64, _vp]),
+    "lcsa_dequantize_entries_fp4": (_i, [ctypes.POINTER(Fp4Entries), _i, _i64, _i, _i, _vp, _i64, _vp, _i, _vp]),
+    "lcsa_attn_fp4_workspace": (_sz, [ctypes.POINTER(AttnArgs), _i]),
+    "lcsa_csa_sparse_attn_fp4": (_i, [ctypes.POINTER(AttnArgs), ctypes.POINTER(Fp4Entries), _vp, _sz, _vp]),
+    "lcsa_hca_dense_attn_fp4": (_i, [ctypes.POINTER(AttnArgs), ctypes.POINTER(Fp4Entries), _vp, _sz, _vp]),
     "lcsa_set_wait_limit_ns": (_i, [ctypes.c_uint64]),
     "lcsa_test_withhold_stage": (None, [_i]),
     "lcsa_set_attn_gather": (_i, [_i]),
@@ -476,3 +488,156 @@ def hca_dense_attn_fp8(q, cache, kv, sink, q_pos0, kv_pos0, m=128, W=128, R=64, 
     """HCA core attention with the entries in the FP8 cache (codes, scales, rope)."""
     return _attn_fp8(_lib.lcsa_hca_dense_attn_fp8, "hca_dense_attn_fp8", 0, q, cache, None, kv, sink, q_pos0,
                      kv_pos0, m, W, R, softmax_scale, rope_base, out_dtype, return_lse, workspace, out)
+
+
+# ----------------------------------------------------------------- FP4 entry cache
+def fp4_scale_bytes(D, R=64):
+    """Bytes of an entry's scale row: one per 32 of its D-R body values, padded to a multiple of 16."""
+    return int(_lib.lcsa_fp4_scale_bytes(D, R))
+
+
+def empty_fp4_cache(B, rows, D=512, R=64, device="cuda"):
+    """An FP4 entry cache of `rows` zero entries per sequence: (codes uint8
+    [B,rows,(D-R)/2], scales uint8 [B,rows,S], rope BF16 [B,rows,R])."""
+    S = fp4_scale_bytes(D, R)
+    if S == 0:
+        raise ValueError("D - R must be a positive multiple of 32 and R a multiple of 8")
+    return (torch.zeros((B, rows, (D - R) // 2), dtype=torch.uint8, device=device),
+            torch.zeros((B, rows, S), dtype=torch.uint8, device=device),
+            torch.zeros((B, rows, R), dtype=torch.bfloat16, device=device))
+
+
+def _fp4_cache(cache, B=None):
+    """The parts of a cache [B,rows,..], checked against each other -> (entries, B, rows, D, R)."""
+    codes, scales, rope = cache
+    _need_contig(codes, scales, rope)
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or rope.dtype != torch.bfloat16:
+        raise TypeError("an FP4 cache is (uint8 codes, uint8 scales, bfloat16 rope)")
+    if codes.dim() != 3 or codes.shape[:2] != scales.shape[:2] or codes.shape[:2] != rope.shape[:2]:
+        raise ValueError("FP4 cache parts must be [B, rows, ..] of the same B and rows")
+    R = rope.shape[2]
+    D = 2 * codes.shape[2] + R
+    if scales.shape[2] != fp4_scale_bytes(D, R) or scales.shape[2] == 0:
+        raise ValueError("FP4 cache parts do not fit together")
+    if B is not None and codes.shape[0] != B:
+        raise ValueError("the FP4 cache holds another number of sequences")
+    _same_device(codes, scales, rope)
+    return Fp4Entries(_p(codes), _p(scales), _p(rope)), codes.shape[0], codes.shape[1], D, R
+
+
+def _same_device(*ts):
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if dev is not None and t.device != dev:
+            raise ValueError("tensors must be on one device")
+        dev = t.device
+    return dev
+
+
+def quantize_entries_fp4(ckv, R=64, cache=None, row0=0):
+    """FP4 entry cache of ckv (BF16 or FP32): MXFP4 codes and scales of the
+    first D-R dims, the last R dims in BF16 -> (codes, scales, rope).
+
+    Without `cache`, ckv [..., D] gives new parts [..., (D-R)/2], [..., S] and
+    [..., R].  With `cache` (parts [B,rows,..]), ckv [B,n,D] is written into
+    rows row0 .. row0+n-1 of every sequence and the cache is returned."""
+    _need_contig(ckv)
+    D = ckv.shape[-1]
+    if cache is None:
+        lead = ckv.shape[:-1]
+        rows = ckv.numel() // D if D else 0
+        flat = empty_fp4_cache(1, rows, D, R, ckv.device)
+        quantize_entries_fp4(ckv.view(1, rows, D), R, cache=flat)
+        return tuple(t.view(lead + t.shape[2:]) for t in flat)
+    if ckv.dim() != 3:
+        raise ValueError("entries written into a cache are [B, n, D]")
+    e, B, rows, Dc, Rc = _fp4_cache(cache, ckv.shape[0])
+    if (Dc, Rc) != (D, R):
+        raise ValueError("the FP4 cache holds entries of another shape")
+    dev = _same_device(ckv, cache[0])
+    with torch.cuda.device(dev):
+        st = _lib.lcsa_quantize_entries_fp4(_p(ckv), B, ckv.shape[1], D, R, _dt(ckv), ctypes.byref(e), rows, int(row0),
+                                            _stream(dev))
+    _check(st, "quantize_entries_fp4")
+    return cache
+
+
+def dequantize_entries_fp4(cache, idx=None, out_dtype=torch.bfloat16, out=None):
+    """Entries read back from an FP4 cache (parts [B,rows,..]): all of them, or
+    rows idx [B,n] int32 of each sequence (-1: a zero row) -> [B,n,D] out_dtype
+    (BF16, or the same values in FP32)."""
+    e, B, rows, D, R = _fp4_cache(cache)
+    if idx is not None:
+        _need_contig(idx)
+        if idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != B:
+            raise ValueError("idx must be int32 [B, n]")
+    n = rows if idx is None else idx.shape[1]
+    if out is None:
+        out = torch.empty((B, n, D), dtype=out_dtype, device=cache[0].device)
+    elif tuple(out.shape) != (B, n, D):
+        raise ValueError("out must be [B, n, D]")
+    _need_contig(out)
+    dev = _same_device(cache[0], idx, out)
+    with torch.cuda.device(dev):
+        st = _lib.lcsa_dequantize_entries_fp4(ctypes.byref(e), B, rows, D, R, _p(idx), n, _p(out), _dt(out),
+                                              _stream(dev))
+    _check(st, "dequantize_entries_fp4")
+    return out
+
+
+def _attn_fp4(fn, name, sparse, q, cache, idx, kv, sink, q_pos0, kv_pos0, m, W, R, softmax_scale, rope_base,
+              out_dtype, return_lse, workspace, out):
+    _need_contig(q, idx, kv, sink)
+    B, Tq, H, D = q.shape
+    e, _, Nc, Dc, Rc = _fp4_cache(cache, B)
+    if (Dc, Rc) != (D, R):
+        raise ValueError("the FP4 cache holds entries of another shape")
+    if kv.dim() != 3 or kv.shape[0] != B or kv.shape[2] != D or kv.dtype != q.dtype:
+        raise ValueError("kv must be [B, Tkv, D] of q's dtype")
+    if idx is not None and (idx.dtype != torch.int32 or idx.dim() != 3 or idx.shape[:2] != q.shape[:2]):
+        raise ValueError("idx must be int32 [B, Tq, k]")
+    if sink is not None and (sink.dtype != torch.float32 or tuple(sink.shape) != (H,)):
+        raise ValueError("sink must be float32 [H]")
+    if out is None:
+        out = torch.empty((B, Tq, H, D), dtype=out_dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _need_contig(out)
+    dev = _same_device(q, cache[0], idx, kv, sink, out, workspace)
+    lse = torch.empty((B, Tq, H), dtype=torch.float32, device=dev) if return_lse else None
+    k = idx.shape[2] if idx is not None else 0
+    a = AttnArgs(_p(q), None, _p(idx), _p(kv), _p(sink), B, Tq, H, D, R, Nc, k, kv.shape[1], int(q_pos0),
+                 int(kv_pos0), m, W, float(softmax_scale), float(rope_base), _dt(q), _p(out), _dt(out), _p(lse))
+    with torch.cuda.device(dev):
+        need = int(_lib.lcsa_attn_fp4_workspace(ctypes.byref(a), sparse))
+        if need > 0 and (workspace is None or workspace.numel() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_n = 0 if workspace is None else workspace.numel()
+        st = fn(ctypes.byref(a), ctypes.byref(e), _p(workspace), ws_n, _stream(dev))
+    _check(st, name)
+    return (out, lse) if return_lse else out
+
+
+def csa_sparse_attn_fp4(q, cache, idx, kv, sink, q_pos0, kv_pos0, m=4, W=128, R=64, softmax_scale=0.0,
+                        rope_base=10000.0, out_dtype=torch.float32, return_lse=False, workspace=None, out=None):
+    """CSA core attention with the entries in the FP4 cache (codes, scales, rope)."""
+    return _attn_fp4(_lib.lcsa_csa_sparse_attn_fp4, "csa_sparse_attn_fp4", 1, q, cache, idx, kv, sink, q_pos0,
+                     kv_pos0, m, W, R, softmax_scale, rope_base, out_dtype, return_lse, workspace, out)
+
+
+def hca_dense_attn_fp4(q, cache, kv, sink, q_pos0, kv_pos0, m=128, W=128, R=64, softmax_scale=0.0,
+                       rope_base=10000.0, out_dtype=torch.float32, return_lse=False, workspace=None, out=None):
+    """HCA core attention with the entries in the FP4 cache (codes, scales, rope)."""
+    return _attn_fp4(_lib.lcsa_hca_dense_attn_fp4, "hca_dense_attn_fp4", 0, q, cache, None, kv, sink, q_pos0,
+                     kv_pos0, m, W, R, softmax_scale, rope_base, out_dtype, return_lse, workspace, out)
+
+
+def attn_fp4_workspace_bytes(q, cache, idx, kv, m, W, R=64, q_pos0=0, kv_pos0=0):
+    """Workspace of csa_sparse_attn_fp4 (idx given) or hca_dense_attn_fp4 (idx None)."""
+    a = AttnArgs(_p(q), None, _p(idx), _p(kv), None, *q.shape, R, cache[0].shape[1], idx.shape[2] if idx is not None else 0,
+                 kv.shape[1], int(q_pos0), int(kv_pos0), m, W, 0.0, 0.0, _dt(q), _p(q), _dt(q), None)
+    return int(_lib.lcsa_attn_fp4_workspace(ctypes.byref(a), 0 if idx is None else 1))

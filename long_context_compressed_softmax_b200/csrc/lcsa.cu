@@ -15,6 +15,7 @@
 #include "attn_tc.cuh"
 #include "indexer_fp4.cuh"
 #include "gemm_tc.cuh"
+#include "fp4cache.cuh"
 
 using namespace lcsa;
 
@@ -520,6 +521,81 @@ lcsa_status lcsa_csa_sparse_attn_fp8(const lcsa_attn_args* a, const lcsa_fp8_ent
 lcsa_status lcsa_hca_dense_attn_fp8(const lcsa_attn_args* a, const lcsa_fp8_entries* e, void* ws, size_t ws_bytes,
                                     void* stream) {
   return attn_fp8_common(a, e, 0, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ FP4 entry cache
+static bool fp4_shape_ok(int D, int R) { return D > 0 && R >= 0 && R % 8 == 0 && D > R && (D - R) % 32 == 0; }
+
+static bool fp4_cache_ok(const lcsa_fp4_entries* c, int R) {
+  return c && c->codes && c->scales && (R == 0 || c->rope) && aligned16(c->codes) && aligned16(c->scales) &&
+         aligned16(c->rope);
+}
+
+size_t lcsa_fp4_scale_bytes(int D, int R) { return fp4_shape_ok(D, R) ? (size_t)fp4_scale_bytes(D, R) : 0; }
+
+lcsa_status lcsa_quantize_entries_fp4(const void* x, int B, int64_t n, int D, int R, lcsa_dtype dtype,
+                                      const lcsa_fp4_entries* cache, int64_t cache_rows, int64_t row0, void* stream) {
+  if (!valid_dtype(dtype) || !fp4_shape_ok(D, R) || B < 0 || n < 0 || cache_rows < 0 || row0 < 0)
+    return LCSA_ERR_INVALID_ARG;
+  if (row0 > cache_rows || n > cache_rows - row0) return LCSA_ERR_INVALID_ARG;
+  if (B == 0 || n == 0) return LCSA_OK;
+  if (!x || !aligned16(x) || !fp4_cache_ok(cache, R)) return LCSA_ERR_INVALID_ARG;
+  if (!have_device()) return LCSA_ERR_CUDA;
+  return from_cuda(launch_quantize_entries_fp4(x, B, n, D, R, dtype, cache, cache_rows, row0, (cudaStream_t)stream));
+}
+
+lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, int64_t cache_rows, int D, int R,
+                                        const int32_t* idx, int64_t n, void* out, lcsa_dtype out_dtype, void* stream) {
+  if (!valid_dtype(out_dtype) || !fp4_shape_ok(D, R) || B < 0 || n < 0 || cache_rows < 0) return LCSA_ERR_INVALID_ARG;
+  if (!idx && n > cache_rows) return LCSA_ERR_INVALID_ARG;
+  if (B == 0 || n == 0) return LCSA_OK;
+  if (!out || !aligned16(out) || (reinterpret_cast<uintptr_t>(idx) & 3u)) return LCSA_ERR_INVALID_ARG;
+  if (cache_rows > 0 && !fp4_cache_ok(cache, R)) return LCSA_ERR_INVALID_ARG;
+  if (!have_device()) return LCSA_ERR_CUDA;
+  const lcsa_fp4_entries none = {nullptr, nullptr, nullptr};
+  return from_cuda(launch_dequantize_entries_fp4(cache_rows > 0 ? cache : &none, B, cache_rows, D, R, idx, n, out,
+                                                 out_dtype, (cudaStream_t)stream));
+}
+
+// The entries in the queries' dtype, then the workspace of the attention over them.
+static size_t fp4_expanded_bytes(const lcsa_attn_args* a) {
+  return align256((size_t)a->B * (size_t)a->Nc * (size_t)a->D * esize(a->dtype));
+}
+
+size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse) {
+  if (!a || a->B <= 0 || a->Tq <= 0 || a->Nc < 0 || a->D <= 0 || !valid_dtype(a->dtype)) return 0;
+  return fp4_expanded_bytes(a) + lcsa_attn_workspace(a, sparse);
+}
+
+static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entries* e, int sparse, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  lcsa_status s = check_attn(a, sparse, 0);
+  if (s != LCSA_OK) return s;
+  if (!fp4_shape_ok(a->D, a->R)) return LCSA_ERR_INVALID_ARG;
+  if ((long long)a->B * a->Tq == 0) return LCSA_OK;
+  if (a->Nc > 0 && !fp4_cache_ok(e, a->R)) return LCSA_ERR_INVALID_ARG;
+  if (!have_device()) return LCSA_ERR_CUDA;
+  const size_t need = lcsa_attn_fp4_workspace(a, sparse);
+  if (need > 0 && (!ws || ws_bytes < need)) return LCSA_ERR_WORKSPACE;
+  if (ws && !aligned16(ws)) return LCSA_ERR_INVALID_ARG;
+  lcsa_attn_args x = *a;
+  x.ckv = ws;
+  if (a->Nc > 0) {
+    cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, a->Nc, ws, a->dtype,
+                                                    (cudaStream_t)stream);
+    if (err != cudaSuccess) return LCSA_ERR_CUDA;
+  }
+  return attn_common(&x, sparse, (char*)ws + fp4_expanded_bytes(a), ws_bytes - fp4_expanded_bytes(a), stream);
+}
+
+lcsa_status lcsa_csa_sparse_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  return attn_fp4_common(a, e, 1, ws, ws_bytes, stream);
+}
+
+lcsa_status lcsa_hca_dense_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  return attn_fp4_common(a, e, 0, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -484,3 +484,30 @@ def dequantize_entries_fp8(codes, scales, rope):
     vals = E4M3_ALL[np.asarray(codes, dtype=np.uint8)]
     X = np.asarray(scales, dtype=np.float64) - 127.0
     return np.concatenate([vals * np.exp2(X)[..., None], np.asarray(rope, dtype=np.float64)], axis=-1)
+
+
+# ----------------------------------------------------------------------------
+# FP4 entry cache  ([p4] "三、FP4量化": E2M1 with block scales; "KV Cache优化细节":
+# the rotary dims stay BF16)
+#
+# Reading (the pages keep entries in FP8 and only indexer keys in FP4): the
+# first D - R dims of an entry in MXFP4 blocks of 32 by the rule of
+# quantize_mxfp4, the last R dims in BF16; scale rows padded with zeros to a
+# multiple of 16 bytes.
+# ----------------------------------------------------------------------------
+def quantize_entries_fp4(ckv, R):
+    """Entries [..., D] -> (codes uint8 [..., (D-R)/2], scales uint8 [..., S],
+    rope BF16 values [..., R] as FP64)."""
+    x = np.asarray(ckv, dtype=np.float64)
+    D = x.shape[-1]
+    codes, scales = quantize_mxfp4(x[..., :D - R])
+    pad = -scales.shape[-1] % 16
+    scales = np.concatenate([scales, np.zeros(scales.shape[:-1] + (pad,), dtype=np.uint8)], axis=-1)
+    return codes, scales, _round_bf16(x[..., D - R:])
+
+
+def dequantize_entries_fp4(codes, scales, rope):
+    """Exact FP64 entries from the FP4 cache: E2M1 value * 2^X, rotary dims as stored."""
+    codes = np.asarray(codes, dtype=np.uint8)
+    body = dequantize_mxfp4(codes, np.asarray(scales)[..., :codes.shape[-1] // 16])
+    return np.concatenate([body, np.asarray(rope, dtype=np.float64)], axis=-1)
