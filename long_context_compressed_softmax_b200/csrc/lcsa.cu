@@ -16,6 +16,7 @@
 #include "indexer_fp4.cuh"
 #include "gemm_tc.cuh"
 #include "fp4cache.cuh"
+#include "attn_fp4.cuh"
 
 using namespace lcsa;
 
@@ -557,14 +558,15 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
                                                  out_dtype, (cudaStream_t)stream));
 }
 
-// The entries in the queries' dtype, then the workspace of the attention over them.
+// Shapes of the CUDA-core kernel only: the entries read back in the queries' dtype.
 static size_t fp4_expanded_bytes(const lcsa_attn_args* a) {
   return align256((size_t)a->B * (size_t)a->Nc * (size_t)a->D * esize(a->dtype));
 }
 
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse) {
+  (void)sparse;
   if (!a || a->B <= 0 || a->Tq <= 0 || a->Nc < 0 || a->D <= 0 || !valid_dtype(a->dtype)) return 0;
-  return fp4_expanded_bytes(a) + lcsa_attn_workspace(a, sparse);
+  return attn_fp4_supported(a) ? 0 : fp4_expanded_bytes(a);
 }
 
 static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entries* e, int sparse, void* ws,
@@ -575,6 +577,7 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
   if ((long long)a->B * a->Tq == 0) return LCSA_OK;
   if (a->Nc > 0 && !fp4_cache_ok(e, a->R)) return LCSA_ERR_INVALID_ARG;
   if (!have_device()) return LCSA_ERR_CUDA;
+  if (attn_fp4_supported(a)) return from_cuda(launch_attn_fp4(a, sparse, e, (cudaStream_t)stream));
   const size_t need = lcsa_attn_fp4_workspace(a, sparse);
   if (need > 0 && (!ws || ws_bytes < need)) return LCSA_ERR_WORKSPACE;
   if (ws && !aligned16(ws)) return LCSA_ERR_INVALID_ARG;
@@ -585,7 +588,7 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
                                                     (cudaStream_t)stream);
     if (err != cudaSuccess) return LCSA_ERR_CUDA;
   }
-  return attn_common(&x, sparse, (char*)ws + fp4_expanded_bytes(a), ws_bytes - fp4_expanded_bytes(a), stream);
+  return from_cuda(launch_attn_generic(&x, sparse, (cudaStream_t)stream));
 }
 
 lcsa_status lcsa_csa_sparse_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* ws, size_t ws_bytes,
