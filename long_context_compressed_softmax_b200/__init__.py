@@ -510,32 +510,48 @@ def empty_fp4_cache(B, rows, D=512, R=64, device="cuda"):
 def _fp4_cache(cache, B=None):
     """The parts of a cache [B,rows,..], checked against each other -> (entries, B, rows, D, R)."""
     codes, scales, rope = cache
-    _need_contig(codes, scales, rope)
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or rope.dtype != torch.bfloat16:
         raise TypeError("an FP4 cache is (uint8 codes, uint8 scales, bfloat16 rope)")
-    if codes.dim() != 3 or codes.shape[:2] != scales.shape[:2] or codes.shape[:2] != rope.shape[:2]:
+    _need_contig(codes, scales, rope)
+    sc, ss, sr = codes.shape, scales.shape, rope.shape
+    if len(sc) != 3 or len(ss) != 3 or len(sr) != 3 or not sc[0] == ss[0] == sr[0] or not sc[1] == ss[1] == sr[1]:
         raise ValueError("FP4 cache parts must be [B, rows, ..] of the same B and rows")
-    R = rope.shape[2]
-    D = 2 * codes.shape[2] + R
-    if scales.shape[2] != fp4_scale_bytes(D, R) or scales.shape[2] == 0:
+    R = sr[2]
+    D = 2 * sc[2] + R
+    if D <= R or R % 8 or (D - R) % 32 or ss[2] != ((D - R) // 32 + 15) // 16 * 16:
         raise ValueError("FP4 cache parts do not fit together")
-    if B is not None and codes.shape[0] != B:
+    if B is not None and sc[0] != B:
         raise ValueError("the FP4 cache holds another number of sequences")
     _same_device(codes, scales, rope)
-    return Fp4Entries(_p(codes), _p(scales), _p(rope)), codes.shape[0], codes.shape[1], D, R
+    return Fp4Entries(codes.data_ptr(), scales.data_ptr(), rope.data_ptr()), sc[0], sc[1], D, R
 
 
 def _same_device(*ts):
-    dev = None
+    """The index of the CUDA device that all the tensors (None: no tensor) are on."""
+    dev = -1
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError("tensors must be on a CUDA device")
-        if dev is not None and t.device != dev:
+        if dev >= 0 and d != dev:
             raise ValueError("tensors must be on one device")
-        dev = t.device
+        dev = d
     return dev
+
+
+def _run(dev, fn, name, *args):
+    """fn(*args, stream) with device `dev` current, on its current stream.  (Host time counts where a kernel takes
+    microseconds: no context object when the device is current already, the stream's handle without its object.)"""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != 0:
+        raise LcsaError(st, name)
 
 
 def quantize_entries_fp4(ckv, R=64, cache=None, row0=0):
@@ -546,8 +562,8 @@ def quantize_entries_fp4(ckv, R=64, cache=None, row0=0):
     [..., R].  With `cache` (parts [B,rows,..]), ckv [B,n,D] is written into
     rows row0 .. row0+n-1 of every sequence and the cache is returned."""
     _need_contig(ckv)
-    D = ckv.shape[-1]
     if cache is None:
+        D = ckv.shape[-1]
         lead = ckv.shape[:-1]
         rows = ckv.numel() // D if D else 0
         flat = empty_fp4_cache(1, rows, D, R, ckv.device)
@@ -555,14 +571,12 @@ def quantize_entries_fp4(ckv, R=64, cache=None, row0=0):
         return tuple(t.view(lead + t.shape[2:]) for t in flat)
     if ckv.dim() != 3:
         raise ValueError("entries written into a cache are [B, n, D]")
-    e, B, rows, Dc, Rc = _fp4_cache(cache, ckv.shape[0])
-    if (Dc, Rc) != (D, R):
+    B, n, D = ckv.shape
+    e, _, rows, Dc, Rc = _fp4_cache(cache, B)
+    if Dc != D or Rc != R:
         raise ValueError("the FP4 cache holds entries of another shape")
-    dev = _same_device(ckv, cache[0])
-    with torch.cuda.device(dev):
-        st = _lib.lcsa_quantize_entries_fp4(_p(ckv), B, ckv.shape[1], D, R, _dt(ckv), ctypes.byref(e), rows, int(row0),
-                                            _stream(dev))
-    _check(st, "quantize_entries_fp4")
+    _run(_same_device(ckv, cache[0]), _lib.lcsa_quantize_entries_fp4, "quantize_entries_fp4", ckv.data_ptr(), B, n, D, R,
+         _dt(ckv), ctypes.byref(e), rows, int(row0))
     return cache
 
 
@@ -571,21 +585,21 @@ def dequantize_entries_fp4(cache, idx=None, out_dtype=torch.bfloat16, out=None):
     rows idx [B,n] int32 of each sequence (-1: a zero row) -> [B,n,D] out_dtype
     (BF16, or the same values in FP32)."""
     e, B, rows, D, R = _fp4_cache(cache)
-    if idx is not None:
+    if idx is None:
+        n = rows
+    else:
         _need_contig(idx)
         if idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != B:
             raise ValueError("idx must be int32 [B, n]")
-    n = rows if idx is None else idx.shape[1]
+        n = idx.shape[1]
     if out is None:
         out = torch.empty((B, n, D), dtype=out_dtype, device=cache[0].device)
     elif tuple(out.shape) != (B, n, D):
         raise ValueError("out must be [B, n, D]")
-    _need_contig(out)
-    dev = _same_device(cache[0], idx, out)
-    with torch.cuda.device(dev):
-        st = _lib.lcsa_dequantize_entries_fp4(ctypes.byref(e), B, rows, D, R, _p(idx), n, _p(out), _dt(out),
-                                              _stream(dev))
-    _check(st, "dequantize_entries_fp4")
+    else:
+        _need_contig(out)
+    _run(_same_device(cache[0], idx, out), _lib.lcsa_dequantize_entries_fp4, "dequantize_entries_fp4", ctypes.byref(e), B,
+         rows, D, R, None if idx is None else idx.data_ptr(), n, out.data_ptr(), _dt(out))
     return out
 
 
@@ -594,31 +608,39 @@ def _attn_fp4(fn, name, sparse, q, cache, idx, kv, sink, q_pos0, kv_pos0, m, W, 
     _need_contig(q, idx, kv, sink)
     B, Tq, H, D = q.shape
     e, _, Nc, Dc, Rc = _fp4_cache(cache, B)
-    if (Dc, Rc) != (D, R):
+    if Dc != D or Rc != R:
         raise ValueError("the FP4 cache holds entries of another shape")
-    if kv.dim() != 3 or kv.shape[0] != B or kv.shape[2] != D or kv.dtype != q.dtype:
+    skv = kv.shape
+    if len(skv) != 3 or skv[0] != B or skv[2] != D or kv.dtype != q.dtype:
         raise ValueError("kv must be [B, Tkv, D] of q's dtype")
-    if idx is not None and (idx.dtype != torch.int32 or idx.dim() != 3 or idx.shape[:2] != q.shape[:2]):
-        raise ValueError("idx must be int32 [B, Tq, k]")
-    if sink is not None and (sink.dtype != torch.float32 or tuple(sink.shape) != (H,)):
-        raise ValueError("sink must be float32 [H]")
+    k, idx_p, sink_p, lse, lse_p = 0, None, None, None, None
+    if idx is not None:
+        si = idx.shape
+        if idx.dtype != torch.int32 or len(si) != 3 or si[0] != B or si[1] != Tq:
+            raise ValueError("idx must be int32 [B, Tq, k]")
+        k, idx_p = si[2], idx.data_ptr()
+    if sink is not None:
+        if sink.dtype != torch.float32 or tuple(sink.shape) != (H,):
+            raise ValueError("sink must be float32 [H]")
+        sink_p = sink.data_ptr()
     if out is None:
         out = torch.empty((B, Tq, H, D), dtype=out_dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    _need_contig(out)
+    else:
+        _need_contig(out)
     dev = _same_device(q, cache[0], idx, kv, sink, out, workspace)
-    lse = torch.empty((B, Tq, H), dtype=torch.float32, device=dev) if return_lse else None
-    k = idx.shape[2] if idx is not None else 0
-    a = AttnArgs(_p(q), None, _p(idx), _p(kv), _p(sink), B, Tq, H, D, R, Nc, k, kv.shape[1], int(q_pos0),
-                 int(kv_pos0), m, W, float(softmax_scale), float(rope_base), _dt(q), _p(out), _dt(out), _p(lse))
-    with torch.cuda.device(dev):
-        need = int(_lib.lcsa_attn_fp4_workspace(ctypes.byref(a), sparse))
-        if need > 0 and (workspace is None or workspace.numel() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_n = 0 if workspace is None else workspace.numel()
-        st = fn(ctypes.byref(a), ctypes.byref(e), _p(workspace), ws_n, _stream(dev))
-    _check(st, name)
+    if return_lse:
+        lse = torch.empty((B, Tq, H), dtype=torch.float32, device=q.device)
+        lse_p = lse.data_ptr()
+    a = AttnArgs(q.data_ptr(), None, idx_p, kv.data_ptr(), sink_p, B, Tq, H, D, R, Nc, k, skv[1], q_pos0, kv_pos0, m, W,
+                 softmax_scale, rope_base, _dt(q), out.data_ptr(), _dt(out), lse_p)
+    pa = ctypes.byref(a)
+    need = _lib.lcsa_attn_fp4_workspace(pa, sparse)
+    if need > 0 and (workspace is None or workspace.numel() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_p, ws_n = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _run(dev, fn, name, pa, ctypes.byref(e), ws_p, ws_n)
     return (out, lse) if return_lse else out
 
 

@@ -4,34 +4,20 @@
 // window of raw BF16 rows, a per-head sink in the denominator, partial RoPE
 // and the -t rotation of the output.
 //
-// Both products run transposed, with the 128 keys of a tile (S) or 128 of the
-// 512 dims (O) on the M side and the 64 heads on the N side:
-//   S^T[128 keys, 64 heads]  = K Q^T          A = K (K-major), B = Q (K-major)
-//   O^T[512 dims, 64 heads] += K^T P^T        A = K^T (MN-major view of the same
-//                                             bytes), B = P^T (MN-major)
-// An M = 64 instruction (64 heads on the M side) runs at half the rate of an
-// M = 128 one, and both take about 45 cycles at N = 64, so a tile of 128 keys
-// costs 64 instructions (2,900 cycles) this way.  O^T takes 256 of the 512
-// tensor memory columns, S^T 64.
+//   out = R(-t) sum_j e^(l_j) k_j / (sum_j e^(l_j) + e^sink),  l_j = scale (R(t) q) . k_j
 //
-// Shared memory: one K tile of 128 keys (128 KB of BF16, 128B-swizzled, eight
-// 64-dim blocks), the queries (64 KB), P (16 KB).  There is no room for a
-// second K tile, so the tile is refilled in four chunks of 128 dims: the
-// product O^T is issued chunk by chunk, each commit frees a chunk, and the
-// producers expand the next tile's codes into it while the later chunks are
-// still being multiplied.  The codes of the next tile (368 bytes a key) wait
-// in the producers' registers, loaded a whole tile ahead.
+// with k_j rotated to its own position.  Tiles of 64 keys, three in flight:
+//   S = Q K^T   M = 64 heads, N = 64 keys, A (the queries) from tensor memory
+//   softmax     two threads a head, the reference moves when a logit exceeds it by 2^8
+//   O += P K    M = 64, N = 2 x 256 dims
+// The 16-bit K tile is made in shared memory from 368 bytes a key: twelve warps
+// expand codes and turn rotary dims while the tiles before are multiplied.
+// Forms with 128 keys or dims on the M side (full-rate MMAs) were measured
+// first and are slower here: with N = 64 both operands' shared-memory reads
+// take the whole bandwidth of shared memory, which the expansion needs too.
 //
-// Softmax with keys on the lanes: a thread holds one key and 32 heads.  The
-// exponent's reference of each head lives in shared memory and moves only when
-// some logit exceeds it by more than 2^8 (one vote per tile); then the column
-// maxima are taken with warp reductions and O^T, whose columns are heads, is
-// rescaled.  Row sums are kept per thread and added up once per query.
-//
-// Warps: 0-7 producers, 8-15 softmax and epilogue, 16 MMA issuer, 17
-// sequencer (the list of tiles: which row each key of a tile is), 18 queries.
-// All follow the sequencer's ring of tile descriptions, so only it knows how
-// queries, selections and windows map to tiles.
+// A sequencer warp turns queries, selections and windows into a ring of tile
+// descriptions that every role follows, so only it knows how they map.
 //
 // Long key lists of few queries are split over the CTAs of a cluster: each
 // leaves its partial O in its shared memory and all of them add up a share of
@@ -39,53 +25,68 @@
 // on timing.
 #pragma once
 #include <atomic>
+#include <cstddef>
 
 #include "tc_ptx.cuh"
 #include "fp4cache.cuh"
 
 namespace lcsa {
 
-constexpr int kF4Keys = 128;                        // keys per tile
-constexpr int kF4ProdWarps = 8, kF4ProdThreads = 256;
-constexpr int kF4SmWarp0 = 8;                       // 8 softmax warps
-constexpr int kF4MmaWarp = 16, kF4SeqWarp = 17, kF4QWarp = 18;
-constexpr int kF4Threads = 19 * 32;
+constexpr int kF4Keys = 64;                         // keys per tile
+constexpr int kF4Stages = 3;
+constexpr int kF4Body = 8, kF4Tail = 4;             // warps that expand codes; that also turn the rotary dims
+// A warp's scheduler is its number mod 4.  The expanding warps keep three of
+// the four schedulers busy; the first is left to the warp that issues the MMAs
+// (whose instructions would otherwise wait their turn behind the expansion),
+// the sequencer, and a quarter of the light roles.  Warps 8 and 12 do nothing.
+constexpr int kF4MmaWarp = 0, kF4SeqWarp = 4;
+constexpr int kF4SmWarp0 = 16;                      // 4 softmax warps
+constexpr int kF4XtWarp0 = 20;                      // 4 transition warps: queries in, outputs out
+constexpr int kF4Threads = 24 * 32;
+constexpr int kF4Readers = kF4Body + kF4Tail + 4 + 4 + 1;   // warps that take every tile description
 constexpr int kF4Ring = 8;                          // tile descriptions in flight
 constexpr int kF4MaxSplits = 16;
-constexpr uint32_t kF4Block = kF4Keys * 128;        // one 64-dim block of the K tile
-constexpr uint32_t kF4QBlock = 64 * 128;            // one 64-dim block of the queries
+constexpr uint32_t kF4Region = 64 * 128;            // 64 keys of 64 dims
+constexpr uint32_t kF4KBytes = 8 * kF4Region;       // a K tile
+constexpr uint32_t kF4PBytes = 64 * 128;
 
 struct F4Tile {
   int32_t row[kF4Keys];      // row of each key within its sequence, -1: no key
   int32_t kind;              // kF4Entries ..
   int32_t first, last;       // of its query (and split)
-  int32_t pad[3];
+  int32_t q_row;             // query row (b * Tq + i)
+  uint32_t mask[2];          // keys that are there
+  int32_t pad[2];
   long long base;            // first row of the sequence in the cache or the raw buffer
   long long pos0, step;      // position of row r: pos0 + r * step
-  long long q_row, t;        // query row (b * Tq + i) and its position
+  long long t;               // position of the query
 };
 constexpr int kF4Entries = 0, kF4Window = 1, kF4Empty = 2, kF4End = 3;
 static_assert(sizeof(F4Tile) % 16 == 0, "tile description");
 
 // shared-memory carve-up, offsets from the 1 KB aligned base
-constexpr uint32_t kF4OffQ = 8 * kF4Block;
-constexpr uint32_t kF4OffP = kF4OffQ + 8 * kF4QBlock;
-constexpr uint32_t kF4OffTab = kF4OffP + kF4Keys * 128;
-constexpr uint32_t kF4OffRef = kF4OffTab + kF4Ring * sizeof(F4Tile);   // [64] reference of each head (log2 units)
-constexpr uint32_t kF4OffNref = kF4OffRef + 64 * 4;                    // [64] minus the reference in use
-constexpr uint32_t kF4OffAlpha = kF4OffNref + 64 * 4;                  // [64]
-constexpr uint32_t kF4OffFac = kF4OffAlpha + 64 * 4;                   // [64] output factor
-constexpr uint32_t kF4OffL = kF4OffFac + 64 * 4;                       // [64] sum of each head (split launches)
-constexpr uint32_t kF4OffWmax = kF4OffL + 64 * 4;                      // [8 warps][32]
-constexpr uint32_t kF4OffWgt = kF4OffWmax + 8 * 32 * 4;                // [splits][64] merge weights
-constexpr uint32_t kF4OffCs = kF4OffWgt + kF4MaxSplits * 64 * 4;       // [32] (cos, sin) of the merge
-constexpr uint32_t kF4OffBar = kF4OffCs + 32 * 8;
-constexpr int kF4Bars = 2 * kF4Ring + 8 + 6;
+constexpr uint32_t kF4OffP = kF4Stages * kF4KBytes;                    // two P tiles
+constexpr uint32_t kF4OffTab = kF4OffP + 2 * kF4PBytes;
+constexpr uint32_t kF4OffStats = kF4OffTab + kF4Ring * sizeof(F4Tile); // [2 items][64] (reference, sum)
+constexpr uint32_t kF4OffRef = kF4OffStats + 2 * 64 * 8;               // [64] of this split
+constexpr uint32_t kF4OffL = kF4OffRef + 64 * 4;                       // [64]
+constexpr uint32_t kF4OffWgt = kF4OffL + 64 * 4;                       // [splits][64] merge weights
+constexpr uint32_t kF4OffCs = kF4OffWgt + kF4MaxSplits * 64 * 4;       // [4 warps][2 items][32] (cos, sin)
+constexpr uint32_t kF4OffTurn = kF4OffCs + 4 * 64 * 8;                 // [32] turns per position
+constexpr uint32_t kF4OffBar = kF4OffTurn + 32 * 8;
+constexpr uint32_t kF4BTabFull = kF4OffBar, kF4BTabEmpty = kF4BTabFull + 8 * kF4Ring;
+constexpr uint32_t kF4BKFull = kF4BTabEmpty + 8 * kF4Ring, kF4BKEmpty = kF4BKFull + 8 * kF4Stages;
+constexpr uint32_t kF4BSFull = kF4BKEmpty + 8 * kF4Stages, kF4BSFree = kF4BSFull + 16, kF4BPFull = kF4BSFree + 16;
+constexpr uint32_t kF4BPvDone = kF4BPFull + 16, kF4BOFree = kF4BPvDone + 16, kF4BStats = kF4BOFree + 16;
+constexpr uint32_t kF4BQReady = kF4BStats + 16, kF4BSDone = kF4BQReady + 8, kF4BDrain = kF4BSDone + 8;
+constexpr int kF4Bars = 2 * kF4Ring + 2 * kF4Stages + 15;
+static_assert(kF4BDrain + 8 == kF4OffBar + 8 * kF4Bars, "barriers");
 constexpr size_t kF4Smem = 1024 + kF4OffBar + kF4Bars * 8;
 static_assert(kF4Smem <= 232448, "FP4 attention shared memory exceeds 227 KB");
 
-// tensor memory: O^T in columns [0, 256), 64 per block of 128 dims; S^T
-constexpr uint32_t kF4TmS = 256;
+// tensor memory: lanes 0-15 of every sub-partition hold S of two tiles (64
+// columns each) and the queries (256 columns), lanes 16-31 O (512 columns)
+constexpr uint32_t kF4TmQ = 128, kF4TmO = 16u << 16;
 
 struct F4Args {
   const uint8_t* codes;
@@ -121,27 +122,10 @@ __device__ __forceinline__ F4Query f4_query(const F4Args& g, long long it) {
   return q;
 }
 
-__device__ __forceinline__ float redux_max(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ float ex2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -179,522 +163,680 @@ __device__ __forceinline__ uint32_t rotate_pair(uint32_t x, float c, float s) {
   return *reinterpret_cast<const uint32_t*>(&o);
 }
 
+// Shared memory by 32-bit address, with constant offsets folded into the access.
+template <int kOff = 0>
+__device__ __forceinline__ uint32_t f4_lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(v) : "r"(a), "n"(kOff) : "memory");
+  return v;
+}
+template <int kOff = 0>
+__device__ __forceinline__ unsigned long long f4_lds64(uint32_t a) {
+  unsigned long long v;
+  asm volatile("ld.shared.u64 %0, [%1 + %2];" : "=l"(v) : "r"(a), "n"(kOff) : "memory");
+  return v;
+}
+template <int kOff = 0>
+__device__ __forceinline__ void f4_sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0 + %1], {%2,%3,%4,%5};" ::"r"(a), "n"(kOff), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+template <int kOff = 0>
+__device__ __forceinline__ void f4_arrive(uint32_t a) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0 + %1];\n\t}" ::"r"(a), "n"(kOff) : "memory");
+}
+template <int kOff>
+__device__ __forceinline__ bool f4_try_wait(uint32_t a, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1 + %2], %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(a), "n"(kOff), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait of a whole warp (the limit and report of tc::mbar_wait).
+template <int kOff = 0>
+__device__ __forceinline__ bool f4_wait(uint32_t a, uint32_t parity) {
+  bool got = f4_try_wait<kOff>(a, parity);
+  if (__all_sync(0xffffffffu, got)) return true;
+  const uint64_t t0 = tc::globaltimer();
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 64 && !got; ++i) got = f4_try_wait<kOff>(a, parity);
+    if (!got && tc::globaltimer() - t0 > tc::wait_limit()) {
+      report(LCSA_DEV_TIMEOUT);
+      break;
+    }
+  } while (!got);
+  return __all_sync(0xffffffffu, got);
+}
+__device__ __forceinline__ uint32_t f4_tile(uint32_t base, int i) {
+  return base + kF4OffTab + (uint32_t)(i % kF4Ring) * (uint32_t)sizeof(F4Tile);
+}
+// The kind of the next description that holds a tile (or is the end), for the
+// expanding warps; its place is ts - 1 afterwards.
+__device__ __forceinline__ int f4_next_tile(uint32_t base, bool& ok, int& ts, int lane) {
+  while (ok) {
+    if (!f4_wait<kF4BTabFull>(base + 8 * (ts % kF4Ring), (ts / kF4Ring) & 1)) {
+      ok = false;
+      break;
+    }
+    const int kind = (int)f4_lds32<offsetof(F4Tile, kind)>(f4_tile(base, ts));
+    ++ts;
+    if (kind != kF4Empty) return kind;
+    __syncwarp();
+    if (lane == 0) f4_arrive<kF4BTabEmpty>(base + 8 * ((ts - 1) % kF4Ring));
+  }
+  return kF4End;
+}
+// A matrix descriptor `off` 16-byte units further: the address field takes the
+// sum (shared memory ends below its limit), one addition of the low word.
+__device__ __forceinline__ uint64_t f4_desc(uint64_t d, uint32_t off) {
+  return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + off);
+}
+// BF16 scale, in both halves, of byte `i` of a word of scale bytes.
+__device__ __forceinline__ uint32_t f4_scale(uint32_t word, int i) { return e8m0_bf16x2((word >> (8 * i)) & 255u); }
+
 __device__ __forceinline__ void f4_cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
 __global__ void __launch_bounds__(kF4Threads, 1)
-attn_fp4_kernel(const __grid_constant__ F4Args g, const __grid_constant__ CUtensorMap tm_q) {
+attn_fp4_kernel(const __grid_constant__ F4Args g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   F4Tile* tab = reinterpret_cast<F4Tile*>(smem + kF4OffTab);
+  float2* s_stats = reinterpret_cast<float2*>(smem + kF4OffStats);
   float* s_ref = reinterpret_cast<float*>(smem + kF4OffRef);
-  float* s_nref = reinterpret_cast<float*>(smem + kF4OffNref);
-  float* s_alpha = reinterpret_cast<float*>(smem + kF4OffAlpha);
-  float* s_fac = reinterpret_cast<float*>(smem + kF4OffFac);
   float* s_l = reinterpret_cast<float*>(smem + kF4OffL);
-  float* s_wmax = reinterpret_cast<float*>(smem + kF4OffWmax);
   float* s_wgt = reinterpret_cast<float*>(smem + kF4OffWgt);
   float2* s_cs = reinterpret_cast<float2*>(smem + kF4OffCs);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kF4OffBar);
-  uint64_t* tab_full = bars;                       // [kF4Ring] sequencer
-  uint64_t* tab_empty = tab_full + kF4Ring;        // [kF4Ring] every role's warps
-  uint64_t* k_full = tab_empty + kF4Ring;          // [4] chunk filled (producer warps)
-  uint64_t* k_empty = k_full + 4;                  // [4] chunk read (MMA commit)
-  uint64_t* s_full = k_empty + 4;                  // MMA commit
-  uint64_t* p_full = s_full + 1;                   // softmax warps
-  uint64_t* q_full = p_full + 1;                   // TMA bytes and the query warp
-  uint64_t* q_empty = q_full + 1;                  // MMA commit after a query's last S
-  uint64_t* o_full = q_empty + 1;                  // MMA commit after a query's last O
-  uint64_t* drain = o_full + 1;                    // MMA commit of an abandoned CTA
+  unsigned long long* s_turn = reinterpret_cast<unsigned long long*>(smem + kF4OffTurn);
+  uint64_t* tab_full = reinterpret_cast<uint64_t*>(smem + kF4BTabFull);     // [kF4Ring] sequencer
+  uint64_t* tab_empty = reinterpret_cast<uint64_t*>(smem + kF4BTabEmpty);   // [kF4Ring] every role's warps
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + kF4BKFull);        // [kF4Stages] expanding warps
+  uint64_t* kv_empty = reinterpret_cast<uint64_t*>(smem + kF4BKEmpty);      // [kF4Stages] MMA commit after O
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + kF4BSFull);         // [2] MMA commit
+  uint64_t* s_free = reinterpret_cast<uint64_t*>(smem + kF4BSFree);         // [2] softmax warps: S is in registers
+  uint64_t* p_full = reinterpret_cast<uint64_t*>(smem + kF4BPFull);         // [2] softmax warps
+  uint64_t* pv_done = reinterpret_cast<uint64_t*>(smem + kF4BPvDone);       // [2] MMA commit
+  uint64_t* o_free = reinterpret_cast<uint64_t*>(smem + kF4BOFree);         // [2] transition warps: half of O has been read
+  uint64_t* stats_full = reinterpret_cast<uint64_t*>(smem + kF4BStats);     // [2] by item, softmax warps
+  uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + kF4BQReady);       // transition warps
+  uint64_t* s_done = reinterpret_cast<uint64_t*>(smem + kF4BSDone);         // MMA commit after an item's last S
+  uint64_t* drain = reinterpret_cast<uint64_t*>(smem + kF4BDrain);          // MMA commit of an abandoned CTA
   __shared__ uint32_t s_tmem;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kF4Ring; ++i) {
       tc::mbar_init(tab_full + i, 1);
-      tc::mbar_init(tab_empty + i, 18);            // 8 producer, 8 softmax, MMA, query warps
+      tc::mbar_init(tab_empty + i, kF4Readers);
     }
-    for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(k_full + i, kF4ProdWarps);
-      tc::mbar_init(k_empty + i, 1);
+    for (int i = 0; i < kF4Stages; ++i) {
+      tc::mbar_init(kv_full + i, kF4Body + kF4Tail);
+      tc::mbar_init(kv_empty + i, 1);
     }
-    tc::mbar_init(s_full, 1);
-    tc::mbar_init(p_full, 8);
-    tc::mbar_init(q_full, 2);
-    tc::mbar_init(q_empty, 1);
-    tc::mbar_init(o_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(s_full + i, 1);
+      tc::mbar_init(s_free + i, 4);
+      tc::mbar_init(p_full + i, 4);
+      tc::mbar_init(pv_done + i, 1);
+      tc::mbar_init(o_free + i, 4);
+      tc::mbar_init(stats_full + i, 4);
+    }
+    tc::mbar_init(q_ready, 4);
+    tc::mbar_init(s_done, 1);
     tc::mbar_init(drain, 1);
     tc::fence_barrier_init();
   }
-  if (threadIdx.x < 64) s_nref[threadIdx.x] = 0.f;
+  if (threadIdx.x < 32) s_turn[threadIdx.x] = g.turn[threadIdx.x];
   if (warp == kF4MmaWarp) { tc::tmem_alloc(&s_tmem, 512); tc::tmem_relinquish(); }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const uint32_t k_base = tc::smem_u32(smem), q_base = k_base + kF4OffQ, p_base = k_base + kF4OffP;
+  const uint32_t k_base = tc::smem_u32(smem), p_base = k_base + kF4OffP;
   const int split = g.splits > 1 ? (int)(blockIdx.x % g.splits) : 0;
 
-  if (warp < kF4ProdWarps) {
-    // ============================================================ producers
-    // Chunk c < 3 of an entry tile is 128 keys x four 32-value blocks: a thread
-    // expands the same block of two keys.  Chunk 3 holds the last two blocks
-    // and the rotary dims (four 16-byte pieces a thread, always the same four
-    // pairs).  Window rows are copied with cp.async, their rotary dims take
-    // the entries' way.
-    const int tid = threadIdx.x;
-    uint4 ca[3][2], cb, rp[4];
-    uint32_t sa[3][2], sb;
+  const int xw = warp < kF4SmWarp0 && (warp & 3) ? 3 * (warp >> 2) + (warp & 3) - 1 : -1;   // expanding warp
+  if (xw >= 0 && xw < kF4Body) {
+    // ============================================================ expanders
+    // Dims 0-383: three 32-value blocks of one key a thread.  Eight keys lie
+    // side by side in a warp, so a store phase writes eight different bank groups.
+    const int tid = 32 * xw + lane;
+    const int key = 8 * xw + (lane & 7), blk = lane >> 3;
+    const uint32_t dst = k_base + (blk >> 1) * kF4Region + key * 128, col0 = (uint32_t)((4 * (blk & 1)) ^ (key & 7)) << 4;
+    // a queue of the next three blocks and their scales (the loop below has
+    // one block's code: unrolled, the roles' code outgrows the instruction cache)
+    uint4 q0, q1, q2;
+    uint32_t w0 = 0, w1 = 0, w2 = 0;
+    const uint4* src = nullptr;
+    uint4 sc = make_uint4(0, 0, 0, 0);
+    bool ok = true;
+    int ts = 0;
+    auto find = [&](uint32_t d, int kind) {                  // a tile's row of this thread's key, its scales
+      const int r = (int)f4_lds32(d + 4 * key);
+      const long long e = (long long)f4_lds64<offsetof(F4Tile, base)>(d) + r;
+      src = nullptr;
+      sc = make_uint4(0, 0, 0, 0);                           // no row: zero codes and scales
+      if (kind == kF4Entries && r >= 0) {
+        src = reinterpret_cast<const uint4*>(g.codes + e * 224) + blk;
+        sc = __ldg(reinterpret_cast<const uint4*>(g.scales) + e);
+      }
+    };
+    auto load = [&](int c) { return src ? __ldg(src + 4 * c) : make_uint4(0, 0, 0, 0); };
+    int kind = f4_next_tile(k_base, ok, ts, lane);
+    if (kind != kF4End) find(f4_tile(k_base, ts - 1), kind);
+    q0 = load(0);
+    q1 = load(1);
+    q2 = load(2);
+    w0 = sc.x; w1 = sc.y; w2 = sc.z;
+    int st = 0;
+    uint32_t par = 1;                                        // of the stage's last reading (none in the first round)
+#pragma unroll 1
+    for (int n = 0; ok && kind != kF4End; ++n) {
+      const uint32_t d = f4_tile(k_base, ts - 1), bar = k_base + 8 * st, buf = st * kF4KBytes;
+      const int slot = (ts - 1) % kF4Ring, cur_kind = kind;
+      kind = f4_next_tile(k_base, ok, ts, lane);
+      src = nullptr;
+      sc = make_uint4(0, 0, 0, 0);
+      if (kind != kF4End) find(f4_tile(k_base, ts - 1), kind);
+      if (!ok || (n >= kF4Stages && !f4_wait<kF4BKEmpty>(bar, par))) { ok = false; break; }
+      if (cur_kind == kF4Entries) {
+        uint32_t to = dst + buf;
+#pragma unroll 1
+        for (int c = 0; c < 3; ++c) {
+          const uint32_t s = f4_scale(w0, blk);
+          f4_sts128(to + col0, e2m1x8_by_products(q0.x, s));
+          f4_sts128(to + (col0 ^ 16), e2m1x8_by_products(q0.y, s));
+          f4_sts128(to + (col0 ^ 32), e2m1x8_by_products(q0.z, s));
+          f4_sts128(to + (col0 ^ 48), e2m1x8_by_products(q0.w, s));
+          q0 = q1;
+          q1 = q2;
+          q2 = load(c);
+          w0 = w1;
+          w1 = w2;
+          w2 = c == 0 ? sc.x : c == 1 ? sc.y : sc.z;
+          to += 2 * kF4Region;
+        }
+      } else {
+        q0 = load(0);
+        q1 = load(1);
+        q2 = load(2);
+        w0 = sc.x; w1 = sc.y; w2 = sc.z;
+        // window rows: 16 pieces of 128 dims a row
+        const long long base = (long long)f4_lds64<offsetof(F4Tile, base)>(d);
+        const int piece = tid & 15;
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
+          const int k = (tid >> 4) + 16 * u, r = (int)f4_lds32(d + 4 * k);
+          const __nv_bfloat16* p = g.kv + (base + (r >= 0 ? r : 0)) * 512 + 8 * piece;
+          const uint32_t to = k_base + buf + (piece >> 3) * kF4Region + k * 128 + (((piece & 7) ^ (k & 7)) << 4);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) f4_cp_async16(to + c * 2 * kF4Region, p + 128 * c, r >= 0 ? 16u : 0u);   // no row: zeros
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        f4_arrive<kF4BKFull>(bar);
+        f4_arrive<kF4BTabEmpty>(k_base + 8 * slot);
+      }
+      if (++st == kF4Stages) { st = 0; par ^= 1; }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");         // nothing may land after the CTA exits
+  } else if (xw >= 0) {
+    // ============================================================ rotary dims
+    // Dims 384-447 (one block of one key a thread) and the rotary dims (four
+    // 16-byte pieces a thread, always the same four pairs), turned to the
+    // keys' positions.
+    const int tid = 32 * (xw - kF4Body) + lane;
+    const int key = 16 * (xw - kF4Body) + (lane & 15), blk = lane >> 4;
+    const uint32_t dst = k_base + 6 * kF4Region + key * 128, col0 = (uint32_t)((4 * blk) ^ (key & 7)) << 4;
+    const uint32_t rdst = k_base + 7 * kF4Region + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
     unsigned long long turn[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) turn[i] = g.turn[4 * (tid & 7) + i];
-    const uint4 zero4 = make_uint4(0, 0, 0, 0);
-
-    auto load_codes = [&](const F4Tile& t, int c) {          // chunk c < 3
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = t.row[(tid >> 2) + 64 * u];
-        ca[c][u] = zero4;
-        sa[c][u] = 127;
-        if (t.kind == kF4Entries && r >= 0) {
-          const long long e = t.base + r;
-          ca[c][u] = __ldg(reinterpret_cast<const uint4*>(g.codes + e * 224) + 4 * c + (tid & 3));
-          sa[c][u] = __ldg(g.scales + e * 16 + 4 * c + (tid & 3));
-        }
+    uint4 q = make_uint4(0, 0, 0, 0), rp[4];
+    uint32_t sc = 0;
+    bool ok = true;
+    int ts = 0;
+    auto load = [&](uint32_t d, int kind) {
+      const bool entries = kind == kF4Entries;
+      const int r = (int)f4_lds32(d + 4 * key);
+      const long long base = (long long)f4_lds64<offsetof(F4Tile, base)>(d), e = base + r;
+      q = make_uint4(0, 0, 0, 0);
+      sc = 0;
+      if (entries && r >= 0) {
+        q = __ldg(reinterpret_cast<const uint4*>(g.codes + e * 224) + 12 + blk);
+        sc = __ldg(g.scales + e * 16 + 12 + blk);
       }
-    };
-    auto load_last = [&](const F4Tile& t) {                  // chunk 3
-      const int r = t.row[tid >> 1];
-      cb = zero4;
-      sb = 127;
-      if (t.kind == kF4Entries && r >= 0) {
-        const long long e = t.base + r;
-        cb = __ldg(reinterpret_cast<const uint4*>(g.codes + e * 224) + 12 + (tid & 1));
-        sb = __ldg(g.scales + e * 16 + 12 + (tid & 1));
-      }
+      const __nv_bfloat16* p = entries ? g.rope : g.kv + 448;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int rr = t.row[(tid >> 3) + 32 * u];
-        rp[u] = zero4;
-        if (rr >= 0) {
-          const long long e = t.base + rr;
-          const __nv_bfloat16* p = t.kind == kF4Entries ? g.rope + e * 64 : g.kv + e * 512 + 448;
-          rp[u] = __ldg(reinterpret_cast<const uint4*>(p) + (tid & 7));
-        }
+        const int rr = (int)f4_lds32(d + 4 * (tid >> 3) + 64 * u);
+        rp[u] = make_uint4(0, 0, 0, 0);
+        if (rr >= 0) rp[u] = __ldg(reinterpret_cast<const uint4*>(p + (base + rr) * (entries ? 64 : 512)) + (tid & 7));
       }
     };
-    auto expand = [&](uint32_t dst, uint4 w, uint32_t scale_byte, int chunk0, int key, bool swap) {
-      // words 0, 2 and 1, 3 change places in half of the lanes, so that the
-      // eight lanes of a store phase write eight different bank groups
-      const uint32_t s2 = e8m0_bf16x2(scale_byte);
-      const uint32_t x[4] = {swap ? w.z : w.x, swap ? w.w : w.y, swap ? w.x : w.z, swap ? w.y : w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ch = chunk0 + (swap ? i ^ 2 : i);
-        tc::sts128(dst + ((uint32_t)(ch ^ (key & 7)) << 4), e2m1x8_to_bf16(x[i], s2));
-      }
-    };
-
-    bool ok = true;
-    int ts = 0;                                              // tile descriptions seen
-    // the next description that holds a tile (or the end); others are returned at once
-    auto next_tile = [&]() -> const F4Tile* {
-      while (true) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(tab_full + ts % kF4Ring, (ts / kF4Ring) & 1))) return nullptr;
-        const F4Tile* t = tab + ts % kF4Ring;
-        if (t->kind != kF4Empty) return t;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tab_empty + ts % kF4Ring);
-        ++ts;
-      }
-    };
-    const F4Tile* cur = next_tile();
-    ok = cur != nullptr;
-    if (ok && cur->kind != kF4End) {
-      load_codes(*cur, 0);
-      load_codes(*cur, 1);
-      load_codes(*cur, 2);
-      load_last(*cur);
-    }
-    for (int n = 0; ok && cur->kind != kF4End; ++n) {
-      const int cur_slot = ts % kF4Ring;
-      ++ts;
-      const F4Tile* nxt = next_tile();
-      if (!nxt) { ok = false; break; }
-      const bool more = nxt->kind != kF4End;
-      const bool window = cur->kind == kF4Window;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (n > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(k_empty + c, (n - 1) & 1))) { ok = false; break; }
-        if (window) {
-          const int nu = c < 3 ? 8 : 4, sh = c < 3 ? 4 : 3;      // c = 3: block 6 only
-          const int piece = tid & ((1 << sh) - 1);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            if (u < nu) {
-              const int key = (tid >> sh) + (kF4ProdThreads >> sh) * u;
-              const int r = cur->row[key];
-              const uint32_t dst = k_base + (2 * c + (piece >> 3)) * kF4Block + key * 128 + (((piece & 7) ^ (key & 7)) << 4);
-              const __nv_bfloat16* src = g.kv + (cur->base + (r >= 0 ? r : 0)) * 512 + 128 * c + 8 * piece;
-              f4_cp_async16(dst, src, r >= 0 ? 16u : 0u);        // no row: zeros
-            }
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-        } else if (c < 3) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int key = (tid >> 2) + 64 * u;
-            expand(k_base + (2 * c + ((tid >> 1) & 1)) * kF4Block + key * 128, ca[c][u], sa[c][u], 4 * (tid & 1), key,
-                   (tid >> 1) & 1);
-          }
-        } else {
-          const int key = tid >> 1;
-          expand(k_base + 6 * kF4Block + key * 128, cb, sb, 4 * (tid & 1), key, false);
-        }
-        if (c == 3) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int key = (tid >> 3) + 32 * u;
-            const unsigned long long pos = (unsigned long long)(cur->pos0 + cur->row[key] * cur->step);
-            uint32_t w[4] = {rp[u].x, rp[u].y, rp[u].z, rp[u].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float cs, sn;
-              turn_cs_fast(pos * turn[i], &cs, &sn);
-              w[i] = rotate_pair(w[i], cs, sn);
-            }
-            tc::sts128(k_base + 7 * kF4Block + key * 128 + (((tid & 7) ^ (key & 7)) << 4),
-                       make_uint4(w[0], w[1], w[2], w[3]));
-          }
-        }
-        if (window) {
-          // a chunk's copies land while the next chunk's are issued
-          if (c > 0) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(k_full + c - 1);
-          }
-          if (c == 3) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(k_full + 3);
-          }
-        } else {
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(k_full + c);
-        }
-        if (more) {
-          if (c < 3) load_codes(*nxt, c);
-          else load_last(*nxt);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tab_empty + cur_slot);
-      cur = nxt;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");         // nothing may land after the CTA exits
-  } else if (warp < kF4MmaWarp) {
-    // ============================================================ softmax
-    const int qd = warp & 3;                                 // tensor memory lanes 32 qd ..
-    const int half = (warp - kF4SmWarp0) >> 2;               // heads 32 half ..
-    const int key = 32 * qd + lane;
-    const int bar_id = 1 + half;                             // the four warps that share these heads
-    const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16) + 32 * half;
-    const uint32_t nref_a = tc::smem_u32(s_nref + 32 * half), alpha_a = tc::smem_u32(s_alpha + 32 * half),
-                   fac_a = tc::smem_u32(s_fac + 32 * half);
-    float l[32];
-#pragma unroll
-    for (int h = 0; h < 32; ++h) l[h] = 0.f;
-    bool fresh = true;                                       // no key of this query seen so far
-    bool ok = true;
-    int n = 0, nq = 0;
-    for (int ts = 0;; ++ts) {
-      if (!__all_sync(0xffffffffu, ok && tc::mbar_wait(tab_full + ts % kF4Ring, (ts / kF4Ring) & 1))) ok = false;
-      int kind = kF4End, last = 0;
-      bool valid = false;
-      long long q_row = 0, t = 0;
-      if (ok) {
-        const F4Tile& d = tab[ts % kF4Ring];
-        kind = d.kind;
-        last = d.last;
-        valid = kind <= kF4Window && d.row[key] >= 0;
-        q_row = d.q_row;
-        t = d.t;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tab_empty + ts % kF4Ring);
-      }
-      // the four warps of a half leave together
-      if (!tc::bar_and(bar_id, 128, ok)) { ok = false; break; }
-      if (kind == kF4End) break;
-      if (kind == kF4Empty) {
-        if (g.splits > 1) {
-          if (qd == 0) {
-            s_ref[32 * half + lane] = -INFINITY;
-            s_l[32 * half + lane] = 0.f;
-          }
-        } else {
-          const long long o0 = q_row * 64 * 512;
-          for (int e = (threadIdx.x - kF4SmWarp0 * 32) * 8; e < 64 * 512; e += 256 * 8) {
-            if (g.out_bf16) {
-              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(g.out) + o0 + e) = make_uint4(0, 0, 0, 0);
-            } else {
-              float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(g.out) + o0 + e);
-              p[0] = p[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-          }
-          if (qd == 0 && g.lse) {
-            const int h = 32 * half + lane;
-            g.lse[q_row * 64 + h] = g.sink ? g.sink[h] : -INFINITY;
-          }
-        }
-        continue;
-      }
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(s_full, n & 1))) ok = false;
-      ++n;
-      tc::tc_fence_after();
-      uint32_t v[32];
-      tc::tmem_ld32(t_lane + kF4TmS, v);
-      tc::tmem_wait_ld_regs32(v);
-      if (!valid) {                                          // weight 0 whatever the reference is
-#pragma unroll
-        for (int h = 0; h < 32; ++h) v[h] = 0xff800000u;
-      }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 r = tc::lds128f(nref_a + 16 * i);
-        mx = fmaxf(mx, fmaf(__uint_as_float(v[4 * i]), g.scale_log2, r.x));
-        mx = fmaxf(mx, fmaf(__uint_as_float(v[4 * i + 1]), g.scale_log2, r.y));
-        mx = fmaxf(mx, fmaf(__uint_as_float(v[4 * i + 2]), g.scale_log2, r.z));
-        mx = fmaxf(mx, fmaf(__uint_as_float(v[4 * i + 3]), g.scale_log2, r.w));
-      }
-      if (bar_or(bar_id, 128, !ok || (valid && (fresh || mx > 8.f)))) {
-        if (!tc::bar_and(bar_id, 128, ok)) { ok = false; break; }
-        // column maxima of this tile: lane h of each warp ends up with head h
-        float mine = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < 32; ++h) {
-          const float r = redux_max(__uint_as_float(v[h]) * g.scale_log2);
-          if (lane == h) mine = r;
-        }
-        const float old = s_ref[32 * half + lane];
-        s_wmax[(4 * half + qd) * 32 + lane] = mine;
-        tc::bar_sync(bar_id, 128);
-        if (qd == 0) {
-          float m = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) m = fmaxf(m, s_wmax[(4 * half + w) * 32 + lane]);
-          float ref = fresh ? m : fmaxf(m, old);
-          if (ref == -INFINITY) ref = 0.f;                   // every logit is -inf or NaN
-          s_alpha[32 * half + lane] = fresh ? 1.f : ex2_ftz(old - ref);
-          s_ref[32 * half + lane] = ref;
-          s_nref[32 * half + lane] = -ref;
-        }
-        tc::bar_sync(bar_id, 128);
-        if (!fresh) {
-          // what has been added up so far follows the new reference; the
-          // product before this S has completed (same issuer, in order)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 a = tc::lds128f(alpha_a + 16 * i);
-            l[4 * i] *= a.x; l[4 * i + 1] *= a.y; l[4 * i + 2] *= a.z; l[4 * i + 3] *= a.w;
-          }
+    int kind = f4_next_tile(k_base, ok, ts, lane);
+    if (kind != kF4End) load(f4_tile(k_base, ts - 1), kind);
+    int st = 0;
+    uint32_t par = 1;
+    for (int n = 0; ok && kind != kF4End; ++n) {
+      const uint32_t d = f4_tile(k_base, ts - 1), bar = k_base + 8 * st, buf = st * kF4KBytes;
+      const int slot = (ts - 1) % kF4Ring, cur_kind = kind;
+      kind = f4_next_tile(k_base, ok, ts, lane);
+      if (!ok) break;
+      const long long pos0 = (long long)f4_lds64<offsetof(F4Tile, pos0)>(d), step = (long long)f4_lds64<offsetof(F4Tile, step)>(d);
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[16];
-            const uint32_t a = t_lane + 64 * (c >> 1) + 16 * (c & 1);
-            tc::tmem_ld16(a, o);
-            tc::tmem_wait_ld_regs16(o);
+      for (int u = 0; u < 4; ++u) {                          // a full turn of the queue: back in order
+        const unsigned long long pos = (unsigned long long)(pos0 + (int)f4_lds32(d + 4 * (tid >> 3) + 64 * u) * step);
+        uint32_t x[4] = {rp[0].x, rp[0].y, rp[0].z, rp[0].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = tc::lds128f(alpha_a + 64 * (c & 1) + 16 * i);
-              o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f.x);
-              o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f.y);
-              o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f.z);
-              o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f.w);
-            }
-            tc::tmem_st16(a, o);
+        for (int i = 0; i < 4; ++i) {
+          float co, si;
+          turn_cs_fast(pos * turn[i], &co, &si);
+          x[i] = rotate_pair(x[i], co, si);
+        }
+        rp[0] = rp[1];
+        rp[1] = rp[2];
+        rp[2] = rp[3];
+        rp[3] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+      const uint32_t s = f4_scale(sc, 0);
+      const uint4 x[4] = {e2m1x8_by_products(q.x, s), e2m1x8_by_products(q.y, s), e2m1x8_by_products(q.z, s),
+                          e2m1x8_by_products(q.w, s)};
+      if (n >= kF4Stages && !f4_wait<kF4BKEmpty>(bar, par)) { ok = false; break; }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f4_sts128(rdst + buf + u * 16 * 128, rp[u]);
+      if (cur_kind == kF4Entries) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f4_sts128(dst + buf + (col0 ^ (i << 4)), x[i]);
+      } else {
+        const long long base = (long long)f4_lds64<offsetof(F4Tile, base)>(d);
+        const int piece = tid & 7;
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
+          const int k = (tid >> 3) + 16 * u, r = (int)f4_lds32(d + 4 * k);
+          f4_cp_async16(k_base + buf + 6 * kF4Region + k * 128 + ((piece ^ (k & 7)) << 4),
+                        g.kv + (base + (r >= 0 ? r : 0)) * 512 + 384 + 8 * piece, r >= 0 ? 16u : 0u);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        f4_arrive<kF4BKFull>(bar);
+        f4_arrive<kF4BTabEmpty>(k_base + 8 * slot);
+      }
+      if (kind != kF4End) load(f4_tile(k_base, ts - 1), kind);
+      if (++st == kF4Stages) { st = 0; par ^= 1; }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= kF4SmWarp0 && warp < kF4XtWarp0) {
+    // ============================================================ softmax
+    // Two threads per head: keys 0-31 and 32-63 of each tile (16x32bx2
+    // accesses of tensor memory lanes 0-15); maxima and sums meet through a shuffle.
+    const int half = lane >> 4, h = 16 * (warp & 3) + (lane & 15);
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t prow = k_base + kF4OffP + h * 128;
+    float m_run = -INFINITY, l_run = 0.f;                    // l_run: this thread's half
+    bool ok = true;
+    int n = 0, ni = 0;
+    for (int ts = 0; ok; ++ts) {
+      if (!f4_wait<kF4BTabFull>(k_base + 8 * (ts % kF4Ring), (ts / kF4Ring) & 1)) break;
+      const uint32_t d = f4_tile(k_base, ts);
+      const int kind = (int)f4_lds32<offsetof(F4Tile, kind)>(d), first = (int)f4_lds32<offsetof(F4Tile, first)>(d),
+                last = (int)f4_lds32<offsetof(F4Tile, last)>(d);
+      const uint32_t mask = f4_lds32<offsetof(F4Tile, mask)>(d + 4 * half);
+      __syncwarp();
+      if (lane == 0) f4_arrive<kF4BTabEmpty>(k_base + 8 * (ts % kF4Ring));
+      if (kind == kF4End) break;
+      if (kind == kF4Empty) continue;
+      const uint32_t sb = n & 1, bar = k_base + 8 * sb;
+      if (!f4_wait<kF4BSFull>(bar, (n >> 1) & 1)) break;
+      tc::tc_fence_after();
+      // twice over S in pieces of 16 keys: for the maximum, then the weights
+      // (little code and few registers; a piece takes some 40 cycles to read)
+      uint32_t v[16];
+      auto logits = [&](int u) {
+        tc::tmem_ld_16x32bx2_x16<32>(t_lane + sb * 64 + 16 * u, v);
+        tc::tmem_wait_ld_regs16(v);
+        const uint32_t m = mask >> (16 * u);
+        if ((m & 0xffffu) != 0xffffu) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!((m >> i) & 1u)) v[i] = 0xff800000u;        // no key: weight 0
+        }
+      };
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        logits(u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * g.scale_log2;
+      float alpha = 1.f;
+      bool grow = false;
+      if (first) {
+        m_run = top;
+        l_run = 0.f;
+      } else if (top > m_run + 8.f) {                        // otherwise weights stay below 2^8
+        alpha = ex2_ftz(m_run - top);
+        m_run = top;
+        grow = true;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        // O follows once the product of the tile before has finished
+        if (!f4_wait<kF4BPvDone>(k_base + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+        tc::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 16) {
+          uint32_t o[16];
+          tc::tmem_ld_16x32bx2_x16<256>(t_lane + kF4TmO + c, o);
+          tc::tmem_wait_ld_regs16(o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tc::tmem_st_16x32bx2_x16<256>(t_lane + kF4TmO + c, o);
+        }
+        tc::tmem_wait_st();
+      }
+      l_run *= alpha;
+      if (n >= 2 && !f4_wait<kF4BPvDone>(bar, ((n >> 1) - 1) & 1)) break;   // P's buffer has been read
+      // weights, rounded to BF16 for the product (2^-9 of a weight, averaged
+      // over the keys); the sums keep the unrounded weights
+      const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        logits(u);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p0 = ex2_ftz(fmaf(__uint_as_float(v[8 * c + 2 * i]), g.scale_log2, neg_m));
+            const float p1 = ex2_ftz(fmaf(__uint_as_float(v[8 * c + 2 * i + 1]), g.scale_log2, neg_m));
+            sum[i] += p0 + p1;
+            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tc::tmem_wait_st();
+          f4_sts128(prow + sb * kF4PBytes + (((4 * half + 2 * u + c) ^ (h & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
         }
-        fresh = false;
       }
-      // weights, their sums, P^T (rounded to BF16 for the product: 2^-9 of a
-      // weight, averaged over the keys; the sums keep the unrounded weights)
-      const uint32_t prow = p_base + key * 128;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 r = tc::lds128f(nref_a + 32 * c + 16 * i);
-          const int h = 8 * c + 4 * i;
-          const float p0 = ex2_ftz(fmaf(__uint_as_float(v[h]), g.scale_log2, r.x));
-          const float p1 = ex2_ftz(fmaf(__uint_as_float(v[h + 1]), g.scale_log2, r.y));
-          const float p2 = ex2_ftz(fmaf(__uint_as_float(v[h + 2]), g.scale_log2, r.z));
-          const float p3 = ex2_ftz(fmaf(__uint_as_float(v[h + 3]), g.scale_log2, r.w));
-          l[h] += p0;
-          l[h + 1] += p1;
-          l[h + 2] += p2;
-          l[h + 3] += p3;
-          const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
-          w[2 * i] = *reinterpret_cast<const uint32_t*>(&b0);
-          w[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b1);
-        }
-        tc::sts128(prow + (((4 * half + c) ^ (key & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) f4_arrive<kF4BSFree>(bar);
+      l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(p_full);
-      if (!last) continue;
-
-      // ---------------------------------------------------------- epilogue
-      // sums over the 32 keys of the warp, head h to lane h, then over the four warps
-#pragma unroll
-      for (int st = 16; st > 0; st >>= 1) {
-        const bool up = lane & st;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < st) {
-            const float send = up ? l[i] : l[i + st];
-            const float mine = up ? l[i + st] : l[i];
-            l[i] = mine + __shfl_xor_sync(0xffffffffu, send, st);
-          }
+      if (lane == 0) f4_arrive<kF4BPFull>(bar);
+      ++n;
+      if (last) {
+        const float l = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+        if (half == 0) s_stats[(ni & 1) * 64 + h] = make_float2(m_run, l);
+        __syncwarp();
+        if (lane == 0) f4_arrive<kF4BStats>(k_base + 8 * (ni & 1));
+        ++ni;
       }
-      s_wmax[(4 * half + qd) * 32 + lane] = l[0];
-      tc::bar_sync(bar_id, 128);
-      if (qd == 0) {
-        const int h = 32 * half + lane;
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += s_wmax[(4 * half + w) * 32 + lane];
-        const float ref = fresh ? -INFINITY : s_ref[h];
-        if (g.splits > 1) {
-          s_ref[h] = ref;
-          s_l[h] = sum;
-        } else {
-          float M = ref, L = sum, f = 1.f;
-          if (g.sink) {
-            const float s2 = g.sink[h] * 1.4426950408889634f;
-            M = fmaxf(ref, s2);
-            f = ref == -INFINITY ? 0.f : exp2f(ref - M);
-            L = sum * f + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
-          }
-          // a row without keys and sink: zero output (a NaN sum stays one)
-          s_fac[h] = L == 0.f ? 0.f : f / L;
-          if (g.lse) g.lse[q_row * 64 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-          s_nref[h] = 0.f;
-        }
-      }
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(o_full, nq & 1))) ok = false;
-      ++nq;
+    }
+  } else if (warp >= kF4XtWarp0) {
+    // ============================================================ transitions
+    // The queries of the next item into tensor memory as soon as the last S of
+    // the item before has completed, then that item's output.  A warp has 16
+    // heads, two threads a head.
+    const int half = lane >> 4, h = 16 * (warp & 3) + (lane & 15);
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    float2* cs = reinterpret_cast<float2*>(smem + kF4OffCs) + (warp & 3) * 64;   // [2 items][32] (cos, sin)
+    bool ok = true;
+    int n = 0, ni = 0, p_row = 0, p_last = 0;
+    auto output = [&](int item) {                            // of the item before
+      ok = f4_wait<kF4BStats>(k_base + 8 * (item & 1), (item >> 1) & 1) && ok;
+      ok = f4_wait<kF4BPvDone>(k_base + 8 * (p_last & 1), (p_last >> 1) & 1) && ok;
       tc::tc_fence_after();
-      tc::bar_sync(bar_id, 128);
+      const float2 ml = s_stats[(item & 1) * 64 + h];        // (reference, sum)
+      float f = 1.f;
       if (g.splits > 1) {
-        // the K tile has been read for the last time: the partial O goes there, [64 heads][512 dims] FP32
-        float* part = reinterpret_cast<float*>(smem);
-#pragma unroll 1
-        for (int mb = 0; mb < 4; ++mb) {
-          tc::tmem_ld32(t_lane + 64 * mb, v);
-          tc::tmem_wait_ld_regs32(v);
-#pragma unroll
-          for (int h = 0; h < 32; ++h) part[(32 * half + h) * 512 + 128 * mb + key] = __uint_as_float(v[h]);
+        if (half == 0) {
+          // (a NaN sum stays one: its weights were taken against 0)
+          s_ref[h] = ml.y == 0.f ? -INFINITY : ml.x == -INFINITY ? 0.f : ml.x;
+          s_l[h] = ml.y;
         }
       } else {
-        float cs = 1.f, sn = 0.f;
-        if (qd >= 2) {
-          turn_cs((unsigned long long)t * g.turn[16 * (qd - 2) + (lane >> 1)], &cs, &sn);
-          if (lane & 1) sn = -sn;                            // x c + y s | y c - x s
+        float M = ml.x, L = ml.y;
+        if (g.sink) {
+          const float sk = g.sink[h] * 1.4426950408889634f;
+          M = fmaxf(ml.x, sk);
+          f = ml.x == -INFINITY ? (L == 0.f ? 0.f : 1.f) : exp2f(ml.x - M);
+          L = L * f + (sk == -INFINITY ? 0.f : exp2f(sk - M));
         }
-#pragma unroll 1
-        for (int mb = 0; mb < 4; ++mb) {
-          tc::tmem_ld32(t_lane + 64 * mb, v);
-          tc::tmem_wait_ld_regs32(v);
-          const bool rot = mb == 3 && qd >= 2;
-          const int d = 128 * mb + key;
+        // a row without keys and sink: zero output (a NaN sum stays one)
+        f = L == 0.f ? 0.f : f / L;
+        if (half == 0 && g.lse) g.lse[(long long)p_row * 64 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      }
+      const float2* c = cs + (item & 1) * 32;
+      uint32_t buf[2][16];
+      tc::tmem_ld_16x32bx2_x16<16>(t_lane + kF4TmO, buf[0]);
+#pragma unroll 2
+      for (int k = 0; k < 16; ++k) {                         // dims 32 k + 16 half ..
+        uint32_t* v = buf[k & 1];
+        tc::tmem_wait_ld_regs16(v);
+        if (k + 1 < 16) tc::tmem_ld_16x32bx2_x16<16>(t_lane + kF4TmO + (k + 1) * 32, buf[(k + 1) & 1]);
+        if (k == 7 || k == 15) {                             // that half of O may be overwritten
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) f4_arrive<kF4BOFree>(k_base + (k == 15 ? 8 : 0));
+        }
+        const int d0 = 32 * k + 16 * half;
+        if (g.splits > 1) {
+          // a split's O goes where the K tiles were, [64 heads][512 dims] FP32, 16-byte pieces xor-ed by head
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 f = tc::lds128f(fac_a + 16 * i);
-            float o[4] = {__uint_as_float(v[4 * i]) * f.x, __uint_as_float(v[4 * i + 1]) * f.y,
-                          __uint_as_float(v[4 * i + 2]) * f.z, __uint_as_float(v[4 * i + 3]) * f.w};
-            if (rot) {
+          for (int i = 0; i < 4; ++i)
+            f4_sts128(k_base + h * 2048 + (((d0 / 4 + i) ^ (h & 7)) << 4), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          continue;
+        }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[j] = fmaf(o[j], cs, __shfl_xor_sync(0xffffffffu, o[j], 1) * sn);
-            }
-            const long long o0 = (q_row * 64 + 32 * half + 4 * i) * 512;
-            if (g.out_bf16) {
-              // even lanes take head 2j (dims d, d+1), odd lanes head 2j+1 (dims d-1, d)
-              __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(g.out) + o0 + (lane & 1 ? 512 + d - 1 : d);
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+        if (k >= 14) {
 #pragma unroll
-              for (int j = 0; j < 4; j += 2) {
-                const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? o[j] : o[j + 1], 1);
-                *reinterpret_cast<__nv_bfloat162*>(out + j * 512) =
-                    lane & 1 ? __floats2bfloat162_rn(got, o[j + 1]) : __floats2bfloat162_rn(o[j], got);
-              }
-            } else {
-              float* out = reinterpret_cast<float*>(g.out) + o0 + d;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) out[j * 512] = o[j];
-            }
+          for (int i = 0; i < 16; i += 2) {
+            const float2 e = c[(d0 - 448 + i) >> 1];         // rotated by -t
+            const float a0 = __uint_as_float(v[i]), a1 = __uint_as_float(v[i + 1]);
+            v[i] = __float_as_uint(a0 * e.x + a1 * e.y);
+            v[i + 1] = __float_as_uint(a1 * e.x - a0 * e.y);
           }
         }
-      }
-      tc::tc_fence_before();                                 // O may be overwritten after the next p_full
-      fresh = true;
+        const long long o0 = ((long long)p_row * 64 + h) * 512 + d0;
+        if (g.out_bf16) {
+          uint32_t w[8];
 #pragma unroll
-      for (int h = 0; h < 32; ++h) l[h] = 0.f;
+          for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(g.out) + o0);
+          o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<float*>(g.out) + o0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+    };
+    for (int ts = 0; ok; ++ts) {
+      if (!f4_wait<kF4BTabFull>(k_base + 8 * (ts % kF4Ring), (ts / kF4Ring) & 1)) break;
+      const uint32_t d = f4_tile(k_base, ts);
+      const int kind = (int)f4_lds32<offsetof(F4Tile, kind)>(d), first = (int)f4_lds32<offsetof(F4Tile, first)>(d),
+                last = (int)f4_lds32<offsetof(F4Tile, last)>(d), q_row = (int)f4_lds32<offsetof(F4Tile, q_row)>(d);
+      const unsigned long long t = f4_lds64<offsetof(F4Tile, t)>(d);
+      __syncwarp();
+      if (lane == 0) f4_arrive<kF4BTabEmpty>(k_base + 8 * (ts % kF4Ring));
+      if (kind == kF4Empty) {
+        // no key at all: the query (or this split of it) contributes nothing
+        if (g.splits > 1) {
+          if (half == 0) {
+            s_ref[h] = -INFINITY;
+            s_l[h] = 0.f;
+          }
+        } else {
+          const long long o0 = ((long long)q_row * 64 + 16 * (warp & 3)) * 512;
+          for (int e = lane * 8; e < 16 * 512; e += 256) {
+            if (g.out_bf16) {
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(g.out) + o0 + e) = make_uint4(0, 0, 0, 0);
+            } else {
+              float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(g.out) + o0 + e);
+              o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+          if (half == 0 && g.lse) g.lse[(long long)q_row * 64 + h] = g.sink ? g.sink[h] : -INFINITY;
+        }
+        continue;
+      }
+      if (kind != kF4End && first) {
+        float c, s;
+        turn_cs(t * s_turn[lane], &c, &s);
+        cs[(ni & 1) * 32 + lane] = make_float2(c, s);
+        __syncwarp();
+        // step k: dims 64 k + 32 half .. to 16 columns (two dims each), 16 further for the second half
+        const uint4* q = reinterpret_cast<const uint4*>(g.q + ((long long)q_row * 64 + h) * 512) + 4 * half;
+        uint4 x[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[0][i] = __ldg(q + i);
+        if (ni > 0 && !f4_wait<kF4BSDone>(k_base, (ni - 1) & 1)) break;    // the last S that read the columns
+        tc::tc_fence_after();
+#pragma unroll 2
+        for (int k = 0; k < 8; ++k) {
+          if (k + 1 < 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[(k + 1) & 1][i] = __ldg(q + 8 * (k + 1) + i);
+          }
+          uint32_t r[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 y = x[k & 1][i];
+            r[4 * i] = y.x; r[4 * i + 1] = y.y; r[4 * i + 2] = y.z; r[4 * i + 3] = y.w;
+          }
+          if (k == 7) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = cs[(ni & 1) * 32 + 16 * half + i];
+              r[i] = rotate_pair(r[i], e.x, e.y);
+            }
+          }
+          tc::tmem_st_16x32bx2_x16<16>(t_lane + kF4TmQ + 32 * k, r);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) f4_arrive<kF4BQReady>(k_base);
+      }
+      if ((kind == kF4End || first) && ni > 0) output(ni - 1);
+      if (kind == kF4End) break;
+      if (first) {
+        ++ni;
+        p_row = q_row;
+      }
+      if (last) p_last = n;
+      ++n;
     }
   } else if (warp == kF4MmaWarp) {
     // ============================================================ MMA issuer
+    // S of the next tile and O of the current one, whichever can go first
+    // (polled without suspending: a suspended wait on one would miss the other).
     if (tc::elect_one()) {
-      const uint32_t idesc_s = tc::idesc_bf16(128, 64, 0, 0);
-      const uint32_t idesc_o = tc::idesc_bf16(128, 64, 1, 1);
-      bool ok = true;
-      int n = 0, nq = 0;
-      for (int ts = 0; ok; ++ts) {
-        if (!tc::mbar_wait(tab_full + ts % kF4Ring, (ts / kF4Ring) & 1)) { ok = false; break; }
-        const F4Tile& d = tab[ts % kF4Ring];
-        const int kind = d.kind, first = d.first, last = d.last;
-        tc::mbar_arrive(tab_empty + ts % kF4Ring);
-        if (kind == kF4End) break;
-        if (kind == kF4Empty) continue;
-        if (first && !tc::mbar_wait(q_full, nq & 1)) { ok = false; break; }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (ok && !tc::mbar_wait(k_full + c, n & 1)) ok = false;
-          if (ok) {
+      const uint32_t idesc_s = tc::idesc_bf16(64, 64, 0, 0);       // A (tensor memory) and B K-major
+      const uint32_t idesc_o = tc::idesc_bf16(64, 256, 0, 1);      // A K-major, B MN-major
+      bool ok = true, have = false;                          // have: tile n - 1 waits for its O
+      int n = 0, st = 0, ni = 0, o_first = 0;
+      uint32_t full_par = 0;
+      const unsigned long long limit = tc::wait_limit();
+      for (int ts = 0; ok;) {
+        int kind, first, last;
+        do {
+          if (!tc::mbar_wait(tab_full + ts % kF4Ring, (ts / kF4Ring) & 1)) { ok = false; break; }
+          const uint32_t d = f4_tile(k_base, ts);
+          kind = (int)f4_lds32<offsetof(F4Tile, kind)>(d);
+          first = (int)f4_lds32<offsetof(F4Tile, first)>(d);
+          last = (int)f4_lds32<offsetof(F4Tile, last)>(d);
+          tc::mbar_arrive(tab_empty + ts % kF4Ring);
+          ++ts;
+        } while (kind == kF4Empty);
+        if (!ok) break;
+        const int b = n & 1, o_st = st == 0 ? kF4Stages - 1 : st - 1;
+        bool s_todo = kind != kF4End;
+        int o_half = 0;                                      // halves of O (dims 0-255, 256-511) already issued
+        unsigned long long t0 = 0;
+        int idle = 0;
+        while (s_todo || have) {
+          bool moved = false;
+          if (s_todo && tc::mbar_test_wait(kv_full + st, full_par) && (n < 2 || tc::mbar_test_wait(s_free + b, ((n >> 1) - 1) & 1)) &&
+              (!first || tc::mbar_test_wait(q_ready, ni & 1))) {
             tc::tc_fence_after();
+            const uint64_t d_k = tc::sdesc_sw128(k_base + st * kF4KBytes, 16, 1024);
+#pragma unroll 4
+            for (int ks = 0; ks < 32; ++ks)
+              tc::mma_bf16_ts(tmem + b * 64, tmem + kF4TmQ + ks * 8,
+                              f4_desc(d_k, ((ks >> 2) * kF4Region + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+            tc::mma_commit(s_full + b);
+            if (last) tc::mma_commit(s_done);
+            s_todo = false;
+            moved = true;
+          }
+          if (have && (o_half > 0 || tc::mbar_test_wait(p_full + (b ^ 1), ((n - 1) >> 1) & 1))) {
+            // the first product of an item overwrites O, so it waits (a half
+            // at a time) for the output of the item before to have been read
+            const int item = ni - 1;                         // of tile n - 1
+            const bool fresh = o_first && item > 0;
+            if (!fresh || tc::mbar_test_wait(o_free + o_half, (item - 1) & 1)) {
+              tc::tc_fence_after();
+              const uint64_t d_p = tc::sdesc_sw128(p_base + (b ^ 1) * kF4PBytes, 16, 1024);
+              const uint64_t d_v = tc::sdesc_sw128(k_base + o_st * kF4KBytes, kF4Region, 1024);
+              const int h1 = fresh && o_half == 0 ? 1 : 2;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t blk = 2 * c + (ks >> 2), off = (ks & 3) * 32;
-              tc::mma_bf16_ss(tmem + kF4TmS, tc::sdesc_sw128(k_base + blk * kF4Block + off, 16, 1024),
-                              tc::sdesc_sw128(q_base + blk * kF4QBlock + off, 16, 1024), idesc_s, c > 0 || ks > 0);
+              for (int hf = 0; hf < 2; ++hf) {
+                if (hf < o_half || hf >= h1) continue;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  tc::mma_bf16_ss(tmem + kF4TmO + hf * 256, f4_desc(d_p, ks * 2),
+                                  f4_desc(d_v, (hf * 4 * kF4Region + ks * 2048) >> 4), idesc_o, !o_first || ks > 0);
+              }
+              o_half = h1;
+              if (o_half == 2) {
+                tc::mma_commit(kv_empty + o_st);
+                tc::mma_commit(pv_done + (b ^ 1));
+                have = false;
+              }
+              moved = true;
+            }
+          }
+          if (moved) {
+            t0 = 0;
+            idle = 0;
+          } else if ((++idle & 255) == 0) {                  // the timer is slow to read: now and then
+            const unsigned long long now = tc::globaltimer();
+            if (t0 == 0) {
+              t0 = now;
+            } else if (now - t0 > limit) {
+              report(LCSA_DEV_TIMEOUT);
+              ok = false;
+              break;
             }
           }
         }
-        if (!ok) break;
-        tc::mma_commit(s_full);
-        if (last) tc::mma_commit(q_empty);
-        if (!tc::mbar_wait(p_full, n & 1)) { ok = false; break; }
-        tc::tc_fence_after();
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            tc::mma_bf16_ss(tmem + 64 * mb, tc::sdesc_sw128(k_base + 2 * mb * kF4Block + ks * 2048, kF4Block, 1024),
-                            tc::sdesc_sw128(p_base + ks * 2048, kF4Block, 1024), idesc_o, !first || ks > 0);
-          tc::mma_commit(k_empty + mb);
-        }
-        if (last) {
-          tc::mma_commit(o_full);
-          ++nq;
-        }
+        if (!ok || kind == kF4End) break;
+        have = true;
+        o_first = first;
+        if (first) ++ni;
         ++n;
+        if (++st == kF4Stages) { st = 0; full_par ^= 1; }
       }
       if (!ok) {                                             // products in flight end before tensor memory is freed
         tc::mma_commit(drain);
@@ -708,7 +850,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g, const __grid_constant__ CUtens
     int ts = 0;
     auto slot_free = [&]() -> bool {
       if (ts >= kF4Ring &&
-          !__all_sync(0xffffffffu, tc::mbar_wait(tab_empty + ts % kF4Ring, ((ts / kF4Ring) - 1) & 1)))
+          !__all_sync(0xffffffffu, tc::mbar_wait_backoff(tab_empty + ts % kF4Ring, ((ts / kF4Ring) - 1) & 1)))
         return false;
       return true;
     };
@@ -747,7 +889,8 @@ attn_fp4_kernel(const __grid_constant__ F4Args g, const __grid_constant__ CUtens
         if (lane == 0) {
           F4Tile& d = tab[ts % kF4Ring];
           d.kind = kF4Empty;
-          d.q_row = q_row;
+          d.first = d.last = 0;
+          d.q_row = (int)q_row;
           d.t = t;
         }
         publish();
@@ -755,10 +898,10 @@ attn_fp4_kernel(const __grid_constant__ F4Args g, const __grid_constant__ CUtens
       }
       for (int tile = t0; tile < t1; ++tile) {
         const bool entries = tile < tiles_c;
-        int row[4];
+        int row[2];
         bool bad = false;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 2; ++u) {
           const int key = lane + 32 * u;
           if (entries) {
             const int e = tile * kF4Keys + key;
@@ -774,64 +917,31 @@ attn_fp4_kernel(const __grid_constant__ F4Args g, const __grid_constant__ CUtens
         if (!slot_free()) { ok = false; break; }
         F4Tile& d = tab[ts % kF4Ring];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) d.row[lane + 32 * u] = row[u];
+        for (int u = 0; u < 2; ++u) d.row[lane + 32 * u] = row[u];
+        const uint32_t m0 = __ballot_sync(0xffffffffu, row[0] >= 0), m1 = __ballot_sync(0xffffffffu, row[1] >= 0);
         if (lane == 0) {
           d.kind = entries ? kF4Entries : kF4Window;
+          d.mask[0] = m0;
+          d.mask[1] = m1;
           d.first = tile == t0;
           d.last = tile == t1 - 1;
           d.base = (long long)b * (entries ? g.Nc : g.Tkv);
           d.pos0 = entries ? 0 : g.kv_pos0;
           d.step = entries ? g.m : 1;
-          d.q_row = q_row;
+          d.q_row = (int)q_row;
           d.t = t;
         }
         publish();
       }
     }
     if (ok && slot_free()) {
-      if (lane == 0) tab[ts % kF4Ring].kind = kF4End;
+      if (lane == 0) {
+        F4Tile& d = tab[ts % kF4Ring];
+        d.kind = kF4End;
+        d.first = d.last = 0;
+      }
       publish();
     }
-  } else {
-    // ============================================================ queries
-    // Dims 0-447 of the 64 heads by TMA, the rotary dims through registers.
-    if (lane == 0) tc::prefetch_tmap(&tm_q);
-    int nq = 0;
-    for (int ts = 0;; ++ts) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(tab_full + ts % kF4Ring, (ts / kF4Ring) & 1))) break;
-      const F4Tile& d = tab[ts % kF4Ring];
-      const int kind = d.kind, first = d.first;
-      const long long q_row = d.q_row, t = d.t;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tab_empty + ts % kF4Ring);
-      if (kind == kF4End) break;
-      if (kind == kF4Empty || !first) continue;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(g.q + q_row * 64 * 512 + 448) + lane;
-      float cs, sn;
-      turn_cs((unsigned long long)t * g.turn[lane], &cs, &sn);
-      if (nq > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(q_empty, (nq - 1) & 1))) break;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(q_full, 7 * kF4QBlock);
-        for (int blk = 0; blk < 7; ++blk)
-          tc::tma_load_2d(smem + kF4OffQ + blk * kF4QBlock, &tm_q, q_full, 64 * blk, (int)(q_row * 64));
-      }
-#pragma unroll 1
-      for (int h0 = 0; h0 < 64; h0 += 32) {
-        uint32_t x[32];
-#pragma unroll
-        for (int h = 0; h < 32; ++h) x[h] = __ldg(src + (h0 + h) * 256);
-#pragma unroll
-        for (int h = 0; h < 32; ++h) {
-          const uint32_t a = q_base + 7 * kF4QBlock + (h0 + h) * 128 + ((((uint32_t)lane >> 2) ^ (h & 7)) << 4) + 4 * (lane & 3);
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(rotate_pair(x[h], cs, sn)) : "memory");
-        }
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(q_full);
-      ++nq;
-    }
-    if (nq > 0) tc::mbar_wait(q_full, (nq - 1) & 1);          // the last copies have landed
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -873,7 +983,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g, const __grid_constant__ CUtens
   const int u1 = 8192 * (split + 1) / S;
   for (int u = 8192 * split / S + threadIdx.x; u < u1; u += kF4Threads) {
     const int h = u >> 7, d = (u & 127) * 4;
-    const uint32_t a = k_base + (uint32_t)u * 16;
+    const uint32_t a = k_base + h * 2048 + (((u & 127) ^ (h & 7)) << 4);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < S; ++r) {
       const float w = s_wgt[r * 64 + h];
@@ -902,6 +1012,24 @@ attn_fp4_kernel(const __grid_constant__ F4Args g, const __grid_constant__ CUtens
 
 static bool attn_fp4_supported(const lcsa_attn_args* a) {
   return a->dtype == LCSA_BF16 && a->H == 64 && a->D == 512 && a->R == 64;
+}
+
+// 64-key tiles of the longest key list.
+static long long attn_fp4_tiles(const lcsa_attn_args* a, int sparse) {
+  const long long nv = (a->q_pos0 + a->Tq - 1) / a->m;
+  const long long n_c = sparse ? a->k : (nv < a->Nc ? nv : a->Nc), n_w = a->W < a->Tkv ? a->W : a->Tkv;
+  return (n_c + kF4Keys - 1) / kF4Keys + (n_w + kF4Keys - 1) / kF4Keys;
+}
+
+// Whether to read the whole cache back once and attend over BF16 entries
+// (attn_tc.cuh) instead of expanding each tile where it is used.  Expanding
+// costs a tile some 0.7 us of an SM (2.3 us a tile here, 1.6 us there); reading
+// back costs 0.33 ns an entry (1.5 KB at 4.6 TB/s) and about 15 us of launches.
+// Measured: 2048 rows of 2176 keys over 8192 entries 1,082 us here and 818 us
+// read back; 64 sequences of one row, 8192 entries each, 175 us and 362 us.
+static bool attn_fp4_expands(const lcsa_attn_args* a, int sparse) {
+  const double rows = (double)a->B * a->Tq;
+  return rows * (double)attn_fp4_tiles(a, sparse) * (0.7 / 148.0) > (double)a->B * a->Nc * 0.33e-3 + 15.0;
 }
 
 // CTAs that run at the same time in clusters of `s`, on the current device
@@ -949,7 +1077,7 @@ static int attn_fp4_splits(long long rows, int tiles) {
     const int slots = attn_fp4_slots(s);
     if (slots <= 0) continue;
     const long long rounds = (rows * s + slots - 1) / slots;
-    const double cost = s == 1 ? rounds * (tiles + 1.0) + 1.0 : rounds * ((tiles + s - 1) / s + 3.0);
+    const double cost = s == 1 ? rounds * (tiles + 2.0) + 3.0 : rounds * ((tiles + s - 1) / s + 7.0);
     if (cost < best_cost * 0.97) {
       best_cost = cost;
       best = s;
@@ -958,9 +1086,26 @@ static int attn_fp4_splits(long long rows, int tiles) {
   return best;
 }
 
+// Turns per position of the 32 rotary pairs, base^(-2i/64) / 2 pi, as 64-bit
+// fractions.  A program has one or two bases: the last one's are kept (32
+// powers take 2 us of host time).
+static void attn_fp4_turns(float base, unsigned long long* turn) {
+  thread_local float last = 0.f;
+  thread_local unsigned long long kept[32];
+  if (base != last) {
+    for (int i = 0; i < 32; ++i) {
+      long double t = powl((long double)base, -(long double)i / 32.0L) * 0.159154943091895335768883763372514362L;
+      t -= floorl(t);
+      kept[i] = (unsigned long long)(t * 18446744073709551616.0L);
+    }
+    last = base;
+  }
+  for (int i = 0; i < 32; ++i) turn[i] = kept[i];
+}
+
 static cudaError_t launch_attn_fp4(const lcsa_attn_args* a, int sparse, const lcsa_fp4_entries* e, cudaStream_t st) {
   const long long rows = (long long)a->B * a->Tq;
-  if (rows > (long long)INT32_MAX / 64) return cudaErrorInvalidValue;       // TMA row coordinates
+  if (rows > (long long)INT32_MAX / kF4MaxSplits) return cudaErrorInvalidValue;   // query rows and CTAs are 32-bit numbers
   F4Args g;
   g.codes = a->Nc > 0 ? e->codes : nullptr;
   g.scales = a->Nc > 0 ? e->scales : nullptr;
@@ -976,25 +1121,13 @@ static cudaError_t launch_attn_fp4(const lcsa_attn_args* a, int sparse, const lc
   g.out_bf16 = a->out_dtype == LCSA_BF16;
   g.rows = rows; g.q_pos0 = a->q_pos0; g.kv_pos0 = a->kv_pos0;
   g.scale_log2 = (a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf(512.f)) * 1.4426950408889634f;
-  const long double base = a->rope_base > 0.f ? (long double)a->rope_base : 10000.0L;
-  for (int i = 0; i < 32; ++i) {
-    long double turn = powl(base, -(long double)i / 32.0L) * 0.159154943091895335768883763372514362L;
-    turn -= floorl(turn);
-    g.turn[i] = (unsigned long long)(turn * 18446744073709551616.0L);
-  }
-  // tiles of the longest key list
-  const long long t_last = a->q_pos0 + a->Tq - 1;
-  long long n_c = t_last / a->m < a->Nc ? t_last / a->m : a->Nc;
-  if (sparse) n_c = a->k;
-  long long n_w = a->W < a->Tkv ? a->W : a->Tkv;
-  const long long tiles = (n_c + kF4Keys - 1) / kF4Keys + (n_w + kF4Keys - 1) / kF4Keys;
+  attn_fp4_turns(a->rope_base > 0.f ? a->rope_base : 10000.f, g.turn);
+  const long long tiles = attn_fp4_tiles(a, sparse);
   cudaError_t err = cudaFuncSetAttribute(attn_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kF4Smem);
   if (err != cudaSuccess) return err;
   err = cudaFuncSetAttribute(attn_fp4_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (err != cudaSuccess) return err;
   g.splits = attn_fp4_splits(rows, (int)(tiles < (1 << 30) ? tiles : (1 << 30)));
-  CUtensorMap m_q;
-  if (!make_tmap_bf16_2d(&m_q, a->q, (uint64_t)rows * 64, 512, 512, 64, 64)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(g.splits > 1 ? (unsigned)(rows * g.splits) : (unsigned)(rows < sm_count() ? rows : sm_count()));
   cfg.blockDim = dim3(kF4Threads);
@@ -1007,7 +1140,7 @@ static cudaError_t launch_attn_fp4(const lcsa_attn_args* a, int sparse, const lc
   cfg.attrs = at;
   cfg.numAttrs = g.splits > 1 ? 1 : 0;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, attn_fp4_kernel, (const F4Args)g, (const CUtensorMap)m_q);
+  return cudaLaunchKernelEx(&cfg, attn_fp4_kernel, (const F4Args)g);
 }
 
 }  // namespace lcsa

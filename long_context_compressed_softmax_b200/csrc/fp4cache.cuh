@@ -70,6 +70,25 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, uint32_t scale2) {
   return o;
 }
 
+// The same for a whole run of words under one scale, with fewer integer
+// operations (they issue at half the rate of a product): the three magnitude
+// bits of a code, put where a BF16 number has its lowest two exponent bits and
+// its highest fraction bit, are the E2M1 number times 2^-126 (the subnormal
+// included), so a product with 2^126 and one with the signed scale finish it.
+// Codes 2i and 2i+1 first move to the same place of the word's two halves.
+__device__ __forceinline__ uint4 e2m1x8_by_products(uint32_t w, uint32_t scale2) {
+  constexpr uint32_t kMag = 0x01C001C0u, kUp = 0x7E807E80u;                        // 2^126
+  uint32_t x = (w & 0xF0F0FFFFu) | ((w << 12) & 0x0F0F0000u);                      // low half: 0 4 2 6
+  x = (x & 0xFFFF0F0Fu) | ((w >> 12) & 0x0000F0F0u);                               // high half: 1 5 3 7
+  const uint32_t d = x >> 6;
+  const uint32_t m[4] = {x << 6, d << 4, x << 2, d}, sg[4] = {x << 12, x << 4, x << 8, x};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = mul_bf16x2(mul_bf16x2(m[i] & kMag, kUp), (sg[i] & 0x80008000u) ^ scale2);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // A warp's lanes are dealt to rows in groups of 2^lg (the smallest power of
 // two that holds a row's 8-value units, at most the whole warp).
 __host__ inline int fp4_row_lanes_log2(int units) {

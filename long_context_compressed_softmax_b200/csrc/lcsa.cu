@@ -558,15 +558,16 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
                                                  out_dtype, (cudaStream_t)stream));
 }
 
-// Shapes of the CUDA-core kernel only: the entries read back in the queries' dtype.
+// The entries read back in the queries' dtype: for the CUDA-core kernel, and
+// for calls whose rows read each entry many times.
 static size_t fp4_expanded_bytes(const lcsa_attn_args* a) {
   return align256((size_t)a->B * (size_t)a->Nc * (size_t)a->D * esize(a->dtype));
 }
 
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse) {
-  (void)sparse;
-  if (!a || a->B <= 0 || a->Tq <= 0 || a->Nc < 0 || a->D <= 0 || !valid_dtype(a->dtype)) return 0;
-  return attn_fp4_supported(a) ? 0 : fp4_expanded_bytes(a);
+  if (!a || a->B <= 0 || a->Tq <= 0 || a->Nc < 0 || a->D <= 0 || a->m <= 0 || !valid_dtype(a->dtype)) return 0;
+  if (attn_fp4_supported(a)) return attn_fp4_expands(a, sparse) ? fp4_expanded_bytes(a) + attn_tc_workspace(a, sparse) : 0;
+  return fp4_expanded_bytes(a);
 }
 
 static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entries* e, int sparse, void* ws,
@@ -577,7 +578,8 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
   if ((long long)a->B * a->Tq == 0) return LCSA_OK;
   if (a->Nc > 0 && !fp4_cache_ok(e, a->R)) return LCSA_ERR_INVALID_ARG;
   if (!have_device()) return LCSA_ERR_CUDA;
-  if (attn_fp4_supported(a)) return from_cuda(launch_attn_fp4(a, sparse, e, (cudaStream_t)stream));
+  if (attn_fp4_supported(a) && !attn_fp4_expands(a, sparse))
+    return from_cuda(launch_attn_fp4(a, sparse, e, (cudaStream_t)stream));
   const size_t need = lcsa_attn_fp4_workspace(a, sparse);
   if (need > 0 && (!ws || ws_bytes < need)) return LCSA_ERR_WORKSPACE;
   if (ws && !aligned16(ws)) return LCSA_ERR_INVALID_ARG;
@@ -588,6 +590,8 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
                                                     (cudaStream_t)stream);
     if (err != cudaSuccess) return LCSA_ERR_CUDA;
   }
+  if (attn_fp4_supported(a))
+    return from_cuda(launch_attn_tc(&x, sparse, (char*)ws + fp4_expanded_bytes(a), (cudaStream_t)stream));
   return from_cuda(launch_attn_generic(&x, sparse, (cudaStream_t)stream));
 }
 
