@@ -21,8 +21,7 @@
 //
 // Long key lists of few queries are split over the CTAs of a cluster: each
 // leaves its partial O in its shared memory and all of them add up a share of
-// it over distributed shared memory, in rank order, so results do not depend
-// on timing.
+// it over distributed shared memory, in a fixed order.
 #pragma once
 #include <atomic>
 #include <cstddef>
@@ -35,10 +34,13 @@ namespace lcsa {
 constexpr int kF4Keys = 64;                         // keys per tile
 constexpr int kF4Stages = 3;
 constexpr int kF4Body = 8, kF4Tail = 4;             // warps that expand codes; that also turn the rotary dims
-// A warp's scheduler is its number mod 4.  The expanding warps keep three of
-// the four schedulers busy; the first is left to the warp that issues the MMAs
-// (whose instructions would otherwise wait their turn behind the expansion),
-// the sequencer, and a quarter of the light roles.  Warps 8 and 12 do nothing.
+// A warp's scheduler is its number mod 4.  The code warps keep three of the
+// four schedulers busy; the first is left to the warp that issues the MMAs
+// (whose instructions would otherwise wait their turn behind the expansion:
+// 1,538 against 1,371 us for 2048 rows of 2176 keys), the sequencer and a
+// quarter of the other roles.  By number, warps 0 to 15: which of the eight
+// code warps (0-7) and four rotary warps (8-11); 15 none.
+constexpr unsigned long long kF4Roles = 0xFBAF9768543F210Full;
 constexpr int kF4MmaWarp = 0, kF4SeqWarp = 4;
 constexpr int kF4SmWarp0 = 16;                      // 4 softmax warps
 constexpr int kF4XtWarp0 = 20;                      // 4 transition warps: queries in, outputs out
@@ -113,10 +115,10 @@ struct F4Query {
   long long row, t;
   int b;
 };
-__device__ __forceinline__ F4Query f4_query(const F4Args& g, long long it) {
+__device__ __forceinline__ F4Query f4_query(const F4Args& g, int it) {
   F4Query q;
-  const int r = (int)(it / g.B);
-  q.b = (int)(it - (long long)r * g.B);
+  const int r = it / g.B;
+  q.b = it - r * g.B;
   q.row = (long long)q.b * g.Tq + g.Tq - 1 - r;
   q.t = g.q_pos0 + g.Tq - 1 - r;
   return q;
@@ -196,15 +198,15 @@ __device__ __forceinline__ bool f4_try_wait(uint32_t a, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait of a whole warp (the limit and report of tc::mbar_wait).
-template <int kOff = 0>
-__device__ __forceinline__ bool f4_wait(uint32_t a, uint32_t parity) {
-  bool got = f4_try_wait<kOff>(a, parity);
-  if (__all_sync(0xffffffffu, got)) return true;
+// Bounded wait of a whole warp (the limit and report of tc::mbar_wait).  The
+// waiting itself is a function: inlined at every wait it adds a tenth to code
+// that is too large for the instruction cache as it is.
+static __device__ __noinline__ bool f4_wait_slow(uint32_t a, uint32_t parity) {
+  bool got = false;
   const uint64_t t0 = tc::globaltimer();
   do {
 #pragma unroll 1
-    for (int i = 0; i < 64 && !got; ++i) got = f4_try_wait<kOff>(a, parity);
+    for (int i = 0; i < 64 && !got; ++i) got = f4_try_wait<0>(a, parity);
     if (!got && tc::globaltimer() - t0 > tc::wait_limit()) {
       report(LCSA_DEV_TIMEOUT);
       break;
@@ -212,6 +214,11 @@ __device__ __forceinline__ bool f4_wait(uint32_t a, uint32_t parity) {
   } while (!got);
   return __all_sync(0xffffffffu, got);
 }
+template <int kOff = 0>
+__device__ __forceinline__ bool f4_wait(uint32_t a, uint32_t parity) {
+  return __all_sync(0xffffffffu, f4_try_wait<kOff>(a, parity)) || f4_wait_slow(a + kOff, parity);
+}
+
 __device__ __forceinline__ uint32_t f4_tile(uint32_t base, int i) {
   return base + kF4OffTab + (uint32_t)(i % kF4Ring) * (uint32_t)sizeof(F4Tile);
 }
@@ -239,8 +246,80 @@ __device__ __forceinline__ uint64_t f4_desc(uint64_t d, uint32_t off) {
 // BF16 scale, in both halves, of byte `i` of a word of scale bytes.
 __device__ __forceinline__ uint32_t f4_scale(uint32_t word, int i) { return e8m0_bf16x2((word >> (8 * i)) & 255u); }
 
+__device__ __forceinline__ void f4_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void f4_cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+// This CTA's share of the merged output: pieces of four dims, kP pieces and kR
+// splits at a time so that eight remote loads are in flight a thread.  Every
+// CTA begins with its own part and goes around from there (an order that does
+// not depend on timing), so no two read the same part at the same time.
+struct F4Merge {
+  const F4Args* g;
+  uint8_t* smem;
+  uint32_t k_base;
+  int split;
+  long long q_row;
+};
+template <int kP, int kR>
+__device__ __forceinline__ void f4_merge(const F4Merge& m) {
+  const F4Args& g = *m.g;
+  const int S = g.splits, u1 = 8192 * (m.split + 1) / S;
+  const float* wgt = reinterpret_cast<const float*>(m.smem + kF4OffWgt);
+  const float2* cs = reinterpret_cast<const float2*>(m.smem + kF4OffCs);
+#pragma unroll 1
+  for (int u0 = 8192 * m.split / S + threadIdx.x; u0 < u1; u0 += kP * kF4Threads) {
+    float4 o[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int r0 = 0; r0 < S; r0 += kR) {
+      float4 x[kP][kR];
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        const int r = m.split + r0 + k < S ? m.split + r0 + k : m.split + r0 + k - S;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          const int u = u0 + i * kF4Threads, h = u >> 7;
+          if (u < u1 && r0 + k < S) x[i][k] = ld_cluster4(cluster_addr(m.k_base + h * 2048 + (((u & 127) ^ (h & 7)) << 4), r));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        const int r = m.split + r0 + k < S ? m.split + r0 + k : m.split + r0 + k - S;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          const int u = u0 + i * kF4Threads;
+          const float w = u < u1 && r0 + k < S ? wgt[r * 64 + (u >> 7)] : 0.f;
+          if (w != 0.f) {                                    // a split without keys left whatever was there
+            o[i].x = fmaf(w, x[i][k].x, o[i].x);
+            o[i].y = fmaf(w, x[i][k].y, o[i].y);
+            o[i].z = fmaf(w, x[i][k].z, o[i].z);
+            o[i].w = fmaf(w, x[i][k].w, o[i].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int u = u0 + i * kF4Threads;
+      if (u >= u1) break;
+      const int h = u >> 7, d = (u & 127) * 4;
+      float4 v = o[i];
+      if (d >= 448) {
+        const float2 e0 = cs[(d - 448) >> 1], e1 = cs[((d - 448) >> 1) + 1];
+        v = make_float4(v.x * e0.x + v.y * e0.y, v.y * e0.x - v.x * e0.y, v.z * e1.x + v.w * e1.y, v.w * e1.x - v.z * e1.y);
+      }
+      const long long at = (m.q_row * 64 + h) * 512 + d;
+      if (g.out_bf16) {
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        store_vec<4>(reinterpret_cast<__nv_bfloat16*>(g.out) + at, f);
+      } else {
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.out) + at) = v;
+      }
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kF4Threads, 1)
@@ -301,8 +380,8 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   const uint32_t k_base = tc::smem_u32(smem), p_base = k_base + kF4OffP;
   const int split = g.splits > 1 ? (int)(blockIdx.x % g.splits) : 0;
 
-  const int xw = warp < kF4SmWarp0 && (warp & 3) ? 3 * (warp >> 2) + (warp & 3) - 1 : -1;   // expanding warp
-  if (xw >= 0 && xw < kF4Body) {
+  const int xw = warp < kF4SmWarp0 ? (int)(kF4Roles >> (4 * warp)) & 15 : 15;               // expanding warp
+  if (xw < kF4Body) {
     // ============================================================ expanders
     // Dims 0-383: three 32-value blocks of one key a thread.  Eight keys lie
     // side by side in a warp, so a store phase writes eight different bank groups.
@@ -389,7 +468,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       if (++st == kF4Stages) { st = 0; par ^= 1; }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");         // nothing may land after the CTA exits
-  } else if (xw >= 0) {
+  } else if (xw < kF4Body + kF4Tail) {
     // ============================================================ rotary dims
     // Dims 384-447 (one block of one key a thread) and the rotary dims (four
     // 16-byte pieces a thread, always the same four pairs), turned to the
@@ -859,38 +938,58 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       if (lane == 0) tc::mbar_arrive(tab_full + ts % kF4Ring);
       ++ts;
     };
-    for (long long it = g.splits > 1 ? blockIdx.x / g.splits : blockIdx.x; ok && it < g.rows; it += step) {
+    for (int it = g.splits > 1 ? (int)blockIdx.x / g.splits : (int)blockIdx.x; ok && it < (int)g.rows; it += step) {
       const F4Query qr = f4_query(g, it);
       const int b = qr.b;
-      const long long q_row = qr.row, t = qr.t;
-      const int32_t* sel = g.sparse ? g.idx + q_row * g.k : nullptr;
-      int n_c;
-      if (g.sparse) {
-        n_c = g.k;
-        if (__ldg(sel + g.k - 1) < 0) {                       // padded: up to the last entry that is not -1
-          int top = 0;
-          for (int e = lane; e < g.k; e += 32)
-            if (__ldg(sel + e) >= 0) top = e + 1;
-          n_c = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
-        }
-      } else {
-        const long long nv = t / g.m;
-        n_c = (int)(nv < g.Nc ? nv : g.Nc);
-      }
+      const long long t = qr.t;
+      const int32_t* sel = g.sparse ? g.idx + qr.row * g.k : nullptr;
       long long wlo = t - g.W + 1, whi = t;
       if (wlo < g.kv_pos0) wlo = g.kv_pos0;
       if (wlo < 0) wlo = 0;
       if (whi > g.kv_pos0 + g.Tkv - 1) whi = g.kv_pos0 + g.Tkv - 1;
-      const int n_w = whi >= wlo ? (int)(whi - wlo + 1) : 0;
-      const int tiles_c = (n_c + kF4Keys - 1) / kF4Keys, tiles = tiles_c + (n_w + kF4Keys - 1) / kF4Keys;
-      const int t0 = (int)((long long)tiles * split / g.splits), t1 = (int)((long long)tiles * (split + 1) / g.splits);
+      const int n_w = whi >= wlo ? (int)(whi - wlo + 1) : 0, w0 = (int)(wlo - g.kv_pos0);
+      int n_c, tiles_c, t0, t1;
+      auto split_tiles = [&](int entries) {                  // this split's share of the key list
+        n_c = entries;
+        tiles_c = (n_c + kF4Keys - 1) / kF4Keys;
+        const unsigned tiles = tiles_c + (n_w + kF4Keys - 1) / kF4Keys;
+        t0 = (int)(tiles * (unsigned)split / (unsigned)g.splits);
+        t1 = (int)(tiles * (unsigned)(split + 1) / (unsigned)g.splits);
+      };
+      // rows of a tile; selected entries are loaded one tile ahead
+      auto rows_of = [&](int tile, int* row) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = lane + 32 * u, e = tile * kF4Keys + key;
+          if (tile < tiles_c) row[u] = e < n_c ? (g.sparse ? __ldg(sel + e) : e) : -1;
+          else row[u] = e - tiles_c * kF4Keys < n_w ? w0 + e - tiles_c * kF4Keys : -1;
+        }
+      };
+      int row[2];
+      if (g.sparse) {
+        // full selections first: whether this one is padded arrives with the first rows
+        const int end = __ldg(sel + g.k - 1);
+        split_tiles(g.k);
+        rows_of(t0, row);
+        if (end < 0) {                                       // up to the last entry that is not -1
+          int top = 0;
+          for (int e = lane; e < g.k; e += 32)
+            if (__ldg(sel + e) >= 0) top = e + 1;
+          split_tiles((int)__reduce_max_sync(0xffffffffu, (unsigned)top));
+          rows_of(t0, row);
+        }
+      } else {
+        const long long nv = ((unsigned long long)t >> 32) ? t / g.m : (long long)((unsigned)t / (unsigned)g.m);
+        split_tiles((int)(nv < g.Nc ? nv : g.Nc));
+        rows_of(t0, row);
+      }
       if (t0 == t1) {
         if (!slot_free()) { ok = false; break; }
         if (lane == 0) {
           F4Tile& d = tab[ts % kF4Ring];
           d.kind = kF4Empty;
           d.first = d.last = 0;
-          d.q_row = (int)q_row;
+          d.q_row = (int)qr.row;
           d.t = t;
         }
         publish();
@@ -898,19 +997,21 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       }
       for (int tile = t0; tile < t1; ++tile) {
         const bool entries = tile < tiles_c;
-        int row[2];
+        const long long base = (long long)b * (entries ? g.Nc : g.Tkv);
+        int next[2] = {-1, -1};
+        if (tile + 1 < t1) rows_of(tile + 1, next);
         bool bad = false;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int key = lane + 32 * u;
-          if (entries) {
-            const int e = tile * kF4Keys + key;
-            row[u] = e < n_c ? (g.sparse ? __ldg(sel + e) : e) : -1;
-            if (row[u] >= g.Nc) { bad = true; row[u] = -1; }
-            if (row[u] < 0) row[u] = -1;
-          } else {
-            const int e = (tile - tiles_c) * kF4Keys + key;
-            row[u] = e < n_w ? (int)(wlo - g.kv_pos0) + e : -1;
+          if (entries && row[u] >= g.Nc) { bad = true; row[u] = -1; }
+          if (row[u] < 0) row[u] = -1;
+          if (entries && row[u] >= 0) {                      // on its way to L2 while the tiles before are worked on
+            const long long e = base + row[u];
+            f4_prefetch(g.codes + e * 224);
+            f4_prefetch(g.codes + e * 224 + 96);
+            f4_prefetch(g.codes + e * 224 + 192);
+            f4_prefetch(g.scales + e * 16);
+            f4_prefetch(g.rope + e * 64);
           }
         }
         if (bad) report(LCSA_DEV_BAD_INDEX);
@@ -925,13 +1026,15 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
           d.mask[1] = m1;
           d.first = tile == t0;
           d.last = tile == t1 - 1;
-          d.base = (long long)b * (entries ? g.Nc : g.Tkv);
+          d.base = base;
           d.pos0 = entries ? 0 : g.kv_pos0;
           d.step = entries ? g.m : 1;
-          d.q_row = (int)q_row;
+          d.q_row = (int)qr.row;
           d.t = t;
         }
         publish();
+        row[0] = next[0];
+        row[1] = next[1];
       }
     }
     if (ok && slot_free()) {
@@ -958,55 +1061,40 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   const int S = g.splits;
   const F4Query qr = f4_query(g, blockIdx.x / S);
   const long long q_row = qr.row, t = qr.t;
+  // every split's references and sums, all loads in flight at once (P's space is free by now)
+  float* s_sum = reinterpret_cast<float*>(smem + kF4OffP);
+  for (int i = threadIdx.x; i < 64 * S; i += kF4Threads) {
+    s_wgt[i] = ld_cluster(cluster_addr(tc::smem_u32(s_ref + (i & 63)), i >> 6));
+    s_sum[i] = ld_cluster(cluster_addr(tc::smem_u32(s_l + (i & 63)), i >> 6));
+  }
+  if (threadIdx.x >= kF4Threads - 32) {
+    const int i = threadIdx.x & 31;
+    float c, s;
+    turn_cs((unsigned long long)t * s_turn[i], &c, &s);
+    s_cs[i] = make_float2(c, s);
+  }
+  __syncthreads();
   if (threadIdx.x < 64) {
     const int h = threadIdx.x;
-    const uint32_t ra = tc::smem_u32(s_ref + h), la = tc::smem_u32(s_l + h);
-    const float s2 = g.sink ? g.sink[h] * 1.4426950408889634f : -INFINITY;
-    float M = s2;
-    for (int r = 0; r < S; ++r) M = fmaxf(M, ld_cluster(cluster_addr(ra, r)));
-    float L = s2 == -INFINITY ? 0.f : exp2f(s2 - M);
+    const float sk = g.sink ? g.sink[h] * 1.4426950408889634f : -INFINITY;
+    float M = sk;
+    for (int r = 0; r < S; ++r) M = fmaxf(M, s_wgt[r * 64 + h]);
+    float L = sk == -INFINITY ? 0.f : exp2f(sk - M);
     for (int r = 0; r < S; ++r) {
-      const float ref = ld_cluster(cluster_addr(ra, r));
+      const float ref = s_wgt[r * 64 + h];
       const float f = ref == -INFINITY ? 0.f : exp2f(ref - M);
       s_wgt[r * 64 + h] = f;
-      L += f == 0.f ? 0.f : f * ld_cluster(cluster_addr(la, r));
+      L += f == 0.f ? 0.f : f * s_sum[r * 64 + h];
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     for (int r = 0; r < S; ++r) s_wgt[r * 64 + h] *= inv;
     if (split == 0 && g.lse) g.lse[q_row * 64 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-  } else if (threadIdx.x < 96) {
-    float c, s;
-    turn_cs((unsigned long long)t * g.turn[threadIdx.x - 64], &c, &s);
-    s_cs[threadIdx.x - 64] = make_float2(c, s);
   }
   __syncthreads();
-  const int u1 = 8192 * (split + 1) / S;
-  for (int u = 8192 * split / S + threadIdx.x; u < u1; u += kF4Threads) {
-    const int h = u >> 7, d = (u & 127) * 4;
-    const uint32_t a = k_base + h * 2048 + (((u & 127) ^ (h & 7)) << 4);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < S; ++r) {
-      const float w = s_wgt[r * 64 + h];
-      if (w != 0.f) {                                        // a split without keys left nothing to read
-        const float4 x = ld_cluster4(cluster_addr(a, r));
-        o.x = fmaf(w, x.x, o.x);
-        o.y = fmaf(w, x.y, o.y);
-        o.z = fmaf(w, x.z, o.z);
-        o.w = fmaf(w, x.w, o.w);
-      }
-    }
-    if (d >= 448) {
-      const float2 e0 = s_cs[(d - 448) >> 1], e1 = s_cs[((d - 448) >> 1) + 1];
-      o = make_float4(o.x * e0.x + o.y * e0.y, o.y * e0.x - o.x * e0.y, o.z * e1.x + o.w * e1.y, o.w * e1.x - o.z * e1.y);
-    }
-    const long long at = (q_row * 64 + h) * 512 + d;
-    if (g.out_bf16) {
-      const float f[4] = {o.x, o.y, o.z, o.w};
-      store_vec<4>(reinterpret_cast<__nv_bfloat16*>(g.out) + at, f);
-    } else {
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.out) + at) = o;
-    }
-  }
+  const F4Merge m = {&g, smem, k_base, split, q_row};
+  if (S >= 8) f4_merge<1, 8>(m);
+  else if (S >= 4) f4_merge<2, 4>(m);
+  else f4_merge<4, 2>(m);
   cluster_sync_all();                                        // no CTA leaves while another reads its part
 }
 
