@@ -33,19 +33,19 @@ namespace lcsa {
 
 constexpr int kF4Keys = 64;                         // keys per tile
 constexpr int kF4Stages = 3;
-constexpr int kF4Body = 8, kF4Tail = 4;             // warps that expand codes; that also turn the rotary dims
-// A warp's scheduler is its number mod 4.  The code warps keep three of the
-// four schedulers busy; the first is left to the warp that issues the MMAs
-// (whose instructions would otherwise wait their turn behind the expansion:
-// 1,538 against 1,371 us for 2048 rows of 2176 keys), the sequencer and a
-// quarter of the other roles.  By number, warps 0 to 15: which of the eight
-// code warps (0-7) and four rotary warps (8-11); 15 none.
-constexpr unsigned long long kF4Roles = 0xFBAF9768543F210Full;
+constexpr int kF4Code = 10, kF4Rot = 4;             // warps that expand codes; that turn the rotary dims
+// A warp's scheduler is its number mod 4.  The expanding warps keep three of
+// the four schedulers busy; the first has fewer of them, for the warp that
+// issues the MMAs (whose instructions would otherwise wait their turn behind
+// the expansion: 1,538 against 1,371 us for 2048 rows of 2176 keys) and the
+// sequencer.  By number, warps 0 to 15: which of the code warps (0-9) and of
+// the rotary warps (10-13); 15 neither.
+constexpr unsigned long long kF4Roles = 0x9DC8B76A543F210Full;
 constexpr int kF4MmaWarp = 0, kF4SeqWarp = 4;
 constexpr int kF4SmWarp0 = 16;                      // 4 softmax warps
 constexpr int kF4XtWarp0 = 20;                      // 4 transition warps: queries in, outputs out
 constexpr int kF4Threads = 24 * 32;
-constexpr int kF4Readers = kF4Body + kF4Tail + 4 + 4 + 1;   // warps that take every tile description
+constexpr int kF4Readers = kF4Code + kF4Rot + 4 + 4 + 1;   // warps that take every tile description
 constexpr int kF4Ring = 8;                          // tile descriptions in flight
 constexpr int kF4MaxSplits = 16;
 constexpr uint32_t kF4Region = 64 * 128;            // 64 keys of 64 dims
@@ -243,9 +243,6 @@ __device__ __forceinline__ int f4_next_tile(uint32_t base, bool& ok, int& ts, in
 __device__ __forceinline__ uint64_t f4_desc(uint64_t d, uint32_t off) {
   return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + off);
 }
-// BF16 scale, in both halves, of byte `i` of a word of scale bytes.
-__device__ __forceinline__ uint32_t f4_scale(uint32_t word, int i) { return e8m0_bf16x2((word >> (8 * i)) & 255u); }
-
 __device__ __forceinline__ void f4_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void f4_cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -355,7 +352,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       tc::mbar_init(tab_empty + i, kF4Readers);
     }
     for (int i = 0; i < kF4Stages; ++i) {
-      tc::mbar_init(kv_full + i, kF4Body + kF4Tail);
+      tc::mbar_init(kv_full + i, kF4Code + kF4Rot);
       tc::mbar_init(kv_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -381,38 +378,38 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   const int split = g.splits > 1 ? (int)(blockIdx.x % g.splits) : 0;
 
   const int xw = warp < kF4SmWarp0 ? (int)(kF4Roles >> (4 * warp)) & 15 : 15;               // expanding warp
-  if (xw < kF4Body) {
-    // ============================================================ expanders
-    // Dims 0-383: three 32-value blocks of one key a thread.  Eight keys lie
-    // side by side in a warp, so a store phase writes eight different bank groups.
-    const int tid = 32 * xw + lane;
-    const int key = 8 * xw + (lane & 7), blk = lane >> 3;
-    const uint32_t dst = k_base + (blk >> 1) * kF4Region + key * 128, col0 = (uint32_t)((4 * (blk & 1)) ^ (key & 7)) << 4;
-    // a queue of the next three blocks and their scales (the loop below has
-    // one block's code: unrolled, the roles' code outgrows the instruction cache)
-    uint4 q0, q1, q2;
-    uint32_t w0 = 0, w1 = 0, w2 = 0;
+  if (xw < kF4Code) {
+    // ============================================================ codes
+    // Warps 0-7: dims 0-383, blocks blk, 4 + blk and 8 + blk of one key a
+    // thread.  Warps 8 and 9: dims 384-447, both blocks of one key a thread.
+    // Eight keys lie side by side in a warp, so a store phase writes eight
+    // different bank groups.
+    const bool wide = xw < 8;
+    const int key = wide ? 8 * xw + (lane & 7) : 32 * (xw - 8) + lane, blk = wide ? lane >> 3 : 0;
+    const int blocks = wide ? 3 : 2, src_step = wide ? 4 : 1;
+    const uint32_t dst_step = wide ? 2 * kF4Region : 0, col_step = wide ? 0 : 64;
+    const uint32_t dst = k_base + (wide ? (uint32_t)(blk >> 1) : 6u) * kF4Region + key * 128;
+    const uint32_t col0 = (uint32_t)((4 * (blk & 1)) ^ (key & 7)) << 4;
+    // this and the next tile's blocks and scales: loaded a tile ahead
+    uint4 q0, q1, q2, n0, n1, n2, sc;
     const uint4* src = nullptr;
-    uint4 sc = make_uint4(0, 0, 0, 0);
     bool ok = true;
     int ts = 0;
-    auto find = [&](uint32_t d, int kind) {                  // a tile's row of this thread's key, its scales
+    auto load = [&](uint32_t d, int kind) {                  // no row: zero codes and scales
       const int r = (int)f4_lds32(d + 4 * key);
-      const long long e = (long long)f4_lds64<offsetof(F4Tile, base)>(d) + r;
-      src = nullptr;
-      sc = make_uint4(0, 0, 0, 0);                           // no row: zero codes and scales
+      n0 = n1 = n2 = sc = make_uint4(0, 0, 0, 0);
       if (kind == kF4Entries && r >= 0) {
-        src = reinterpret_cast<const uint4*>(g.codes + e * 224) + blk;
+        const long long e = (long long)f4_lds64<offsetof(F4Tile, base)>(d) + r;
+        src = reinterpret_cast<const uint4*>(g.codes + e * 224) + (wide ? blk : 12);
         sc = __ldg(reinterpret_cast<const uint4*>(g.scales) + e);
+        n0 = __ldg(src);
+        n1 = __ldg(src + src_step);
+        if (wide) n2 = __ldg(src + 8);
       }
     };
-    auto load = [&](int c) { return src ? __ldg(src + 4 * c) : make_uint4(0, 0, 0, 0); };
     int kind = f4_next_tile(k_base, ok, ts, lane);
-    if (kind != kF4End) find(f4_tile(k_base, ts - 1), kind);
-    q0 = load(0);
-    q1 = load(1);
-    q2 = load(2);
-    w0 = sc.x; w1 = sc.y; w2 = sc.z;
+    n0 = n1 = n2 = sc = make_uint4(0, 0, 0, 0);
+    if (kind != kF4End) load(f4_tile(k_base, ts - 1), kind);
     int st = 0;
     uint32_t par = 1;                                        // of the stage's last reading (none in the first round)
 #pragma unroll 1
@@ -420,42 +417,37 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       const uint32_t d = f4_tile(k_base, ts - 1), bar = k_base + 8 * st, buf = st * kF4KBytes;
       const int slot = (ts - 1) % kF4Ring, cur_kind = kind;
       kind = f4_next_tile(k_base, ok, ts, lane);
-      src = nullptr;
-      sc = make_uint4(0, 0, 0, 0);
-      if (kind != kF4End) find(f4_tile(k_base, ts - 1), kind);
+      q0 = n0;
+      q1 = n1;
+      q2 = n2;
+      uint32_t w0 = wide ? sc.x >> (8 * blk) : sc.w, w1 = wide ? sc.y >> (8 * blk) : sc.w >> 8, w2 = sc.z >> (8 * blk);
+      if (kind != kF4End) load(f4_tile(k_base, ts - 1), kind);
       if (!ok || (n >= kF4Stages && !f4_wait<kF4BKEmpty>(bar, par))) { ok = false; break; }
       if (cur_kind == kF4Entries) {
-        uint32_t to = dst + buf;
+        uint32_t to = dst + buf, col = col0;
 #pragma unroll 1
-        for (int c = 0; c < 3; ++c) {
-          const uint32_t s = f4_scale(w0, blk);
-          f4_sts128(to + col0, e2m1x8_by_products(q0.x, s));
-          f4_sts128(to + (col0 ^ 16), e2m1x8_by_products(q0.y, s));
-          f4_sts128(to + (col0 ^ 32), e2m1x8_by_products(q0.z, s));
-          f4_sts128(to + (col0 ^ 48), e2m1x8_by_products(q0.w, s));
+        for (int c = 0; c < blocks; ++c) {                   // one block's code: unrolled, the roles' code
+          const uint32_t s = e8m0_bf16x2(w0 & 255u);         // outgrows the instruction cache
+          f4_sts128(to + col, e2m1x8_by_products(q0.x, s));
+          f4_sts128(to + (col ^ 16), e2m1x8_by_products(q0.y, s));
+          f4_sts128(to + (col ^ 32), e2m1x8_by_products(q0.z, s));
+          f4_sts128(to + (col ^ 48), e2m1x8_by_products(q0.w, s));
           q0 = q1;
           q1 = q2;
-          q2 = load(c);
           w0 = w1;
           w1 = w2;
-          w2 = c == 0 ? sc.x : c == 1 ? sc.y : sc.z;
-          to += 2 * kF4Region;
+          to += dst_step;
+          col ^= col_step;
         }
       } else {
-        q0 = load(0);
-        q1 = load(1);
-        q2 = load(2);
-        w0 = sc.x; w1 = sc.y; w2 = sc.z;
-        // window rows: 16 pieces of 128 dims a row
+        // window rows, 16 bytes at a time: 48 pieces a row for the first eight warps, 8 for the others
         const long long base = (long long)f4_lds64<offsetof(F4Tile, base)>(d);
-        const int piece = tid & 15;
+        const int first = wide ? 32 * xw + lane : 32 * (xw - 8) + lane, row = wide ? 48 : 8, p0 = wide ? 0 : 48;
 #pragma unroll 1
-        for (int u = 0; u < 4; ++u) {
-          const int k = (tid >> 4) + 16 * u, r = (int)f4_lds32(d + 4 * k);
-          const __nv_bfloat16* p = g.kv + (base + (r >= 0 ? r : 0)) * 512 + 8 * piece;
-          const uint32_t to = k_base + buf + (piece >> 3) * kF4Region + k * 128 + (((piece & 7) ^ (k & 7)) << 4);
-#pragma unroll
-          for (int c = 0; c < 3; ++c) f4_cp_async16(to + c * 2 * kF4Region, p + 128 * c, r >= 0 ? 16u : 0u);   // no row: zeros
+        for (int i = first; i < 64 * row; i += wide ? 256 : 64) {
+          const int k = i / row, piece = p0 + i - k * row, r = (int)f4_lds32(d + 4 * k);
+          f4_cp_async16(k_base + buf + (piece >> 3) * kF4Region + k * 128 + (((piece & 7) ^ (k & 7)) << 4),
+                        g.kv + (base + (r >= 0 ? r : 0)) * 512 + 8 * piece, r >= 0 ? 16u : 0u);   // no row: zeros
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
@@ -468,49 +460,41 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       if (++st == kF4Stages) { st = 0; par ^= 1; }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");         // nothing may land after the CTA exits
-  } else if (xw < kF4Body + kF4Tail) {
+  } else if (xw < kF4Code + kF4Rot) {
     // ============================================================ rotary dims
-    // Dims 384-447 (one block of one key a thread) and the rotary dims (four
-    // 16-byte pieces a thread, always the same four pairs), turned to the
-    // keys' positions.
-    const int tid = 32 * (xw - kF4Body) + lane;
-    const int key = 16 * (xw - kF4Body) + (lane & 15), blk = lane >> 4;
-    const uint32_t dst = k_base + 6 * kF4Region + key * 128, col0 = (uint32_t)((4 * blk) ^ (key & 7)) << 4;
-    const uint32_t rdst = k_base + 7 * kF4Region + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
+    // Four 16-byte pieces a thread, always of the same four pairs, turned to
+    // the keys' positions.
+    const int tid = 32 * (xw - kF4Code) + lane;
+    const uint32_t dst = k_base + 7 * kF4Region + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
     unsigned long long turn[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) turn[i] = g.turn[4 * (tid & 7) + i];
-    uint4 q = make_uint4(0, 0, 0, 0), rp[4];
-    uint32_t sc = 0;
+    uint4 nr[4];                                             // of the next tile, loaded a tile ahead
     bool ok = true;
     int ts = 0;
     auto load = [&](uint32_t d, int kind) {
-      const bool entries = kind == kF4Entries;
-      const int r = (int)f4_lds32(d + 4 * key);
-      const long long base = (long long)f4_lds64<offsetof(F4Tile, base)>(d), e = base + r;
-      q = make_uint4(0, 0, 0, 0);
-      sc = 0;
-      if (entries && r >= 0) {
-        q = __ldg(reinterpret_cast<const uint4*>(g.codes + e * 224) + 12 + blk);
-        sc = __ldg(g.scales + e * 16 + 12 + blk);
-      }
-      const __nv_bfloat16* p = entries ? g.rope : g.kv + 448;
+      const __nv_bfloat16* p = (kind == kF4Entries ? g.rope : g.kv + 448) + 8 * (tid & 7);
+      const int ld = kind == kF4Entries ? 64 : 512;
+      const long long base = (long long)f4_lds64<offsetof(F4Tile, base)>(d);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int rr = (int)f4_lds32(d + 4 * (tid >> 3) + 64 * u);
-        rp[u] = make_uint4(0, 0, 0, 0);
-        if (rr >= 0) rp[u] = __ldg(reinterpret_cast<const uint4*>(p + (base + rr) * (entries ? 64 : 512)) + (tid & 7));
+        const int r = (int)f4_lds32(d + 4 * (tid >> 3) + 64 * u);
+        nr[u] = make_uint4(0, 0, 0, 0);
+        if (r >= 0) nr[u] = __ldg(reinterpret_cast<const uint4*>(p + (base + r) * ld));
       }
     };
     int kind = f4_next_tile(k_base, ok, ts, lane);
     if (kind != kF4End) load(f4_tile(k_base, ts - 1), kind);
     int st = 0;
     uint32_t par = 1;
+#pragma unroll 1
     for (int n = 0; ok && kind != kF4End; ++n) {
       const uint32_t d = f4_tile(k_base, ts - 1), bar = k_base + 8 * st, buf = st * kF4KBytes;
-      const int slot = (ts - 1) % kF4Ring, cur_kind = kind;
+      const int slot = (ts - 1) % kF4Ring;
       kind = f4_next_tile(k_base, ok, ts, lane);
       if (!ok) break;
+      uint4 rp[4] = {nr[0], nr[1], nr[2], nr[3]};
+      if (kind != kF4End) load(f4_tile(k_base, ts - 1), kind);
       const long long pos0 = (long long)f4_lds64<offsetof(F4Tile, pos0)>(d), step = (long long)f4_lds64<offsetof(F4Tile, step)>(d);
 #pragma unroll 1
       for (int u = 0; u < 4; ++u) {                          // a full turn of the queue: back in order
@@ -527,36 +511,17 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         rp[2] = rp[3];
         rp[3] = make_uint4(x[0], x[1], x[2], x[3]);
       }
-      const uint32_t s = f4_scale(sc, 0);
-      const uint4 x[4] = {e2m1x8_by_products(q.x, s), e2m1x8_by_products(q.y, s), e2m1x8_by_products(q.z, s),
-                          e2m1x8_by_products(q.w, s)};
       if (n >= kF4Stages && !f4_wait<kF4BKEmpty>(bar, par)) { ok = false; break; }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) f4_sts128(rdst + buf + u * 16 * 128, rp[u]);
-      if (cur_kind == kF4Entries) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f4_sts128(dst + buf + (col0 ^ (i << 4)), x[i]);
-      } else {
-        const long long base = (long long)f4_lds64<offsetof(F4Tile, base)>(d);
-        const int piece = tid & 7;
-#pragma unroll 1
-        for (int u = 0; u < 4; ++u) {
-          const int k = (tid >> 3) + 16 * u, r = (int)f4_lds32(d + 4 * k);
-          f4_cp_async16(k_base + buf + 6 * kF4Region + k * 128 + ((piece ^ (k & 7)) << 4),
-                        g.kv + (base + (r >= 0 ? r : 0)) * 512 + 384 + 8 * piece, r >= 0 ? 16u : 0u);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-      }
+      for (int u = 0; u < 4; ++u) f4_sts128(dst + buf + u * 16 * 128, rp[u]);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         f4_arrive<kF4BKFull>(bar);
         f4_arrive<kF4BTabEmpty>(k_base + 8 * slot);
       }
-      if (kind != kF4End) load(f4_tile(k_base, ts - 1), kind);
       if (++st == kF4Stages) { st = 0; par ^= 1; }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kF4SmWarp0 && warp < kF4XtWarp0) {
     // ============================================================ softmax
     // Two threads per head: keys 0-31 and 32-63 of each tile (16x32bx2
