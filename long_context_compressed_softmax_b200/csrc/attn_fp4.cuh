@@ -243,7 +243,6 @@ __device__ __forceinline__ int f4_next_tile(uint32_t base, bool& ok, int& ts, in
 __device__ __forceinline__ uint64_t f4_desc(uint64_t d, uint32_t off) {
   return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + off);
 }
-__device__ __forceinline__ void f4_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void f4_cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
@@ -970,14 +969,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         for (int u = 0; u < 2; ++u) {
           if (entries && row[u] >= g.Nc) { bad = true; row[u] = -1; }
           if (row[u] < 0) row[u] = -1;
-          if (entries && row[u] >= 0) {                      // on its way to L2 while the tiles before are worked on
-            const long long e = base + row[u];
-            f4_prefetch(g.codes + e * 224);
-            f4_prefetch(g.codes + e * 224 + 96);
-            f4_prefetch(g.codes + e * 224 + 192);
-            f4_prefetch(g.scales + e * 16);
-            f4_prefetch(g.rope + e * 64);
-          }
         }
         if (bad) report(LCSA_DEV_BAD_INDEX);
         if (!slot_free()) { ok = false; break; }
