@@ -749,24 +749,19 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         cs[(ni & 1) * 32 + lane] = make_float2(c, s);
         __syncwarp();
         // step k: dims 64 k + 32 half .. to 16 columns (two dims each), 16 further for the second half
-        const uint4* q = reinterpret_cast<const uint4*>(g.q + ((long long)q_row * 64 + h) * 512) + 4 * half;
-        uint4 x[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[0][i] = __ldg(q + i);
+        // (64 bytes a thread and step; 32-byte loads halve the requests, whose
+        // number is what this takes)
+        const __nv_bfloat16* q = g.q + ((long long)q_row * 64 + h) * 512 + 32 * half;
+        const bool wide = (reinterpret_cast<uintptr_t>(g.q) & 31u) == 0;
+        uint32_t x[3][16];                                   // loads two steps ahead
+        ld_words<2>(q, x[0], wide);
+        ld_words<2>(q + 64, x[1], wide);
         if (ni > 0 && !f4_wait<kF4BSDone>(k_base, (ni - 1) & 1)) break;    // the last S that read the columns
         tc::tc_fence_after();
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
-          if (k + 1 < 8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[(k + 1) & 1][i] = __ldg(q + 8 * (k + 1) + i);
-          }
-          uint32_t r[16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 y = x[k & 1][i];
-            r[4 * i] = y.x; r[4 * i + 1] = y.y; r[4 * i + 2] = y.z; r[4 * i + 3] = y.w;
-          }
+          if (k + 2 < 8) ld_words<2>(q + 64 * (k + 2), x[(k + 2) % 3], wide);
+          uint32_t* r = x[k % 3];
           if (k == 7) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
