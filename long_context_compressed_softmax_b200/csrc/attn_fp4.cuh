@@ -100,7 +100,7 @@ struct F4Args {
   const float* sink;
   void* out;
   float* lse;
-  int B, Tq, Nc, k, Tkv, m, W;
+  int B, Tq, n_q, Nc, k, Tkv, m, W;      // the first n_q of Tq rows of every sequence
   int sparse, splits, out_bf16;
   long long rows, q_pos0, kv_pos0;
   float scale_log2;
@@ -119,8 +119,8 @@ __device__ __forceinline__ F4Query f4_query(const F4Args& g, int it) {
   F4Query q;
   const int r = it / g.B;
   q.b = it - r * g.B;
-  q.row = (long long)q.b * g.Tq + g.Tq - 1 - r;
-  q.t = g.q_pos0 + g.Tq - 1 - r;
+  q.row = (long long)q.b * g.Tq + g.n_q - 1 - r;
+  q.t = g.q_pos0 + g.n_q - 1 - r;
   return q;
 }
 
@@ -1053,22 +1053,25 @@ static bool attn_fp4_supported(const lcsa_attn_args* a) {
   return a->dtype == LCSA_BF16 && a->H == 64 && a->D == 512 && a->R == 64;
 }
 
-// 64-key tiles of the longest key list.
-static long long attn_fp4_tiles(const lcsa_attn_args* a, int sparse) {
-  const long long nv = (a->q_pos0 + a->Tq - 1) / a->m;
+// 64-key tiles of the longest key list of the first n_q rows.
+static long long attn_fp4_tiles(const lcsa_attn_args* a, int sparse, int n_q) {
+  const long long nv = (a->q_pos0 + n_q - 1) / a->m;
   const long long n_c = sparse ? a->k : (nv < a->Nc ? nv : a->Nc), n_w = a->W < a->Tkv ? a->W : a->Tkv;
   return (n_c + kF4Keys - 1) / kF4Keys + (n_w + kF4Keys - 1) / kF4Keys;
 }
 
 // Whether to read the whole cache back once and attend over BF16 entries
 // (attn_tc.cuh) instead of expanding each tile where it is used.  Expanding
-// costs a tile some 0.7 us of an SM (2.3 us a tile here, 1.6 us there); reading
-// back costs 0.33 ns an entry (1.5 KB at 4.6 TB/s) and about 15 us of launches.
-// Measured: 2048 rows of 2176 keys over 8192 entries 1,082 us here and 818 us
-// read back; 64 sequences of one row, 8192 entries each, 175 us and 362 us.
+// costs a tile some 0.25 us of an SM; reading back costs 0.33 ns an entry
+// (1.5 KB at 4.6 TB/s) and about 15 us of launches.  Measured: 2048 rows of
+// 2176 keys over 8192 entries 936 us here and 805 us read back, 2048 rows of
+// 1152 keys over 1024 entries 529 and 381 us; 64 sequences of one row, 8192
+// entries each, 139 us and 362 us.  That kernel multiplies whole tiles, masked
+// keys by a weight of zero, so a window has to end with its tile and be in kv.
 static bool attn_fp4_expands(const lcsa_attn_args* a, int sparse) {
+  if (a->W % kF4Keys != 0 || (a->W > 0 && a->kv_pos0 + a->Tkv < a->q_pos0 + a->Tq)) return false;
   const double rows = (double)a->B * a->Tq;
-  return rows * (double)attn_fp4_tiles(a, sparse) * (0.7 / 148.0) > (double)a->B * a->Nc * 0.33e-3 + 15.0;
+  return rows * (double)attn_fp4_tiles(a, sparse, a->Tq) * (0.25 / 148.0) > (double)a->B * a->Nc * 0.33e-3 + 15.0;
 }
 
 // CTAs that run at the same time in clusters of `s`, on the current device
@@ -1142,9 +1145,10 @@ static void attn_fp4_turns(float base, unsigned long long* turn) {
   for (int i = 0; i < 32; ++i) turn[i] = kept[i];
 }
 
-static cudaError_t launch_attn_fp4(const lcsa_attn_args* a, int sparse, const lcsa_fp4_entries* e, cudaStream_t st) {
-  const long long rows = (long long)a->B * a->Tq;
-  if (rows > (long long)INT32_MAX / kF4MaxSplits) return cudaErrorInvalidValue;   // query rows and CTAs are 32-bit numbers
+// The first n_q rows of every sequence.
+static cudaError_t launch_attn_fp4(const lcsa_attn_args* a, int sparse, const lcsa_fp4_entries* e, cudaStream_t st, int n_q) {
+  const long long rows = (long long)a->B * n_q;
+  if ((long long)a->B * a->Tq > (long long)INT32_MAX / kF4MaxSplits) return cudaErrorInvalidValue;   // 32-bit row and CTA numbers
   F4Args g;
   g.codes = a->Nc > 0 ? e->codes : nullptr;
   g.scales = a->Nc > 0 ? e->scales : nullptr;
@@ -1155,13 +1159,13 @@ static cudaError_t launch_attn_fp4(const lcsa_attn_args* a, int sparse, const lc
   g.sink = a->sink;
   g.out = a->out;
   g.lse = a->lse;
-  g.B = a->B; g.Tq = a->Tq; g.Nc = a->Nc; g.k = a->k; g.Tkv = a->Tkv; g.m = a->m; g.W = a->W;
+  g.B = a->B; g.Tq = a->Tq; g.n_q = n_q; g.Nc = a->Nc; g.k = a->k; g.Tkv = a->Tkv; g.m = a->m; g.W = a->W;
   g.sparse = sparse;
   g.out_bf16 = a->out_dtype == LCSA_BF16;
   g.rows = rows; g.q_pos0 = a->q_pos0; g.kv_pos0 = a->kv_pos0;
   g.scale_log2 = (a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf(512.f)) * 1.4426950408889634f;
   attn_fp4_turns(a->rope_base > 0.f ? a->rope_base : 10000.f, g.turn);
-  const long long tiles = attn_fp4_tiles(a, sparse);
+  const long long tiles = attn_fp4_tiles(a, sparse, n_q);
   cudaError_t err = cudaFuncSetAttribute(attn_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kF4Smem);
   if (err != cudaSuccess) return err;
   err = cudaFuncSetAttribute(attn_fp4_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

@@ -245,15 +245,16 @@ static cudaError_t launch_quantize_entries_fp4(const void* x, int B, long long n
 // ---------------------------------------------------------------------------
 // Reading the cache back: row r of sequence b is entry idx[b, r] (entry r
 // without idx); -1 gives a zero row, any other index outside [0, cache_rows)
-// a zero row and LCSA_DEV_BAD_INDEX.  Mostly the 2 D (4 D) bytes written per
+// a zero row and LCSA_DEV_BAD_INDEX; so does, unreported, an entry from
+// live_rows on (entries that nobody is to see, whatever they hold).  Mostly the 2 D (4 D) bytes written per
 // row.  A block a lane, as above (131,072 selected rows of 512 values to BF16:
 // 49.0 us with 8 values a lane, 43.2 us with 32).
 // ---------------------------------------------------------------------------
 template <typename To>
 __global__ void __launch_bounds__(256)
 dequantize_entries_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                              const __nv_bfloat16* __restrict__ rope, long long cache_rows, int D, int R, int lg, bool wide,
-                              const int32_t* __restrict__ idx, long long n, long long rows, To* __restrict__ out) {
+                              const __nv_bfloat16* __restrict__ rope, long long cache_rows, long long live_rows, int D, int R,
+                              int lg, bool wide, const int32_t* __restrict__ idx, long long n, long long rows, To* __restrict__ out) {
   constexpr int kOut = sizeof(To) / 2;                                  // 32-byte pieces of 16 values
   const int lane = threadIdx.x & 31;
   const int body = D - R, nblk = body >> 5, pieces = fp4_pieces(D, R);
@@ -264,8 +265,8 @@ dequantize_entries_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* 
   for (long long r = group0; r < rows; r += groups) {
     const Fp4Row at = fp4_row(r, n);
     const long long e = idx ? (long long)__ldg(idx + r) : at.i;
-    const bool there = e >= 0 && e < cache_rows;
-    if (!there && e != -1 && ul == 0) report(LCSA_DEV_BAD_INDEX);
+    const bool there = e >= 0 && e < live_rows;
+    if ((e < -1 || e >= cache_rows) && ul == 0) report(LCSA_DEV_BAD_INDEX);
     const long long src = at.b * cache_rows + e;
     for (int p = ul; p < pieces; p += 1 << lg) {
       To* to = out + r * D + 32 * p;
@@ -318,18 +319,18 @@ dequantize_entries_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* 
 
 static cudaError_t launch_dequantize_entries_fp4(const lcsa_fp4_entries* c, int B, long long cache_rows, int D, int R,
                                                  const int32_t* idx, long long n, void* out, lcsa_dtype odt,
-                                                 cudaStream_t st) {
+                                                 cudaStream_t st, long long live_rows) {
   const long long rows = (long long)B * n;
   const int lg = fp4_row_lanes_log2(fp4_pieces(D, R)), threads = fp4_block_threads(rows, lg), grid = fp4_grid(rows, lg, threads);
   const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && D % (odt == LCSA_BF16 ? 16 : 8) == 0;
   count_launch();
   if (odt == LCSA_BF16)
     dequantize_entries_fp4_kernel<__nv_bfloat16><<<grid, threads, 0, st>>>(c->codes, c->scales, (const __nv_bfloat16*)c->rope,
-                                                                       cache_rows, D, R, lg, wide, idx, n, rows,
+                                                                       cache_rows, live_rows, D, R, lg, wide, idx, n, rows,
                                                                        (__nv_bfloat16*)out);
   else
     dequantize_entries_fp4_kernel<float><<<grid, threads, 0, st>>>(c->codes, c->scales, (const __nv_bfloat16*)c->rope,
-                                                               cache_rows, D, R, lg, wide, idx, n, rows, (float*)out);
+                                                               cache_rows, live_rows, D, R, lg, wide, idx, n, rows, (float*)out);
   return cudaGetLastError();
 }
 

@@ -555,7 +555,7 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
   if (!have_device()) return LCSA_ERR_CUDA;
   const lcsa_fp4_entries none = {nullptr, nullptr, nullptr};
   return from_cuda(launch_dequantize_entries_fp4(cache_rows > 0 ? cache : &none, B, cache_rows, D, R, idx, n, out,
-                                                 out_dtype, (cudaStream_t)stream));
+                                                 out_dtype, (cudaStream_t)stream, cache_rows));
 }
 
 // The entries read back in the queries' dtype: for the CUDA-core kernel, and
@@ -579,20 +579,25 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
   if (a->Nc > 0 && !fp4_cache_ok(e, a->R)) return LCSA_ERR_INVALID_ARG;
   if (!have_device()) return LCSA_ERR_CUDA;
   if (attn_fp4_supported(a) && !attn_fp4_expands(a, sparse))
-    return from_cuda(launch_attn_fp4(a, sparse, e, (cudaStream_t)stream));
+    return from_cuda(launch_attn_fp4(a, sparse, e, (cudaStream_t)stream, a->Tq));
   const size_t need = lcsa_attn_fp4_workspace(a, sparse);
   if (need > 0 && (!ws || ws_bytes < need)) return LCSA_ERR_WORKSPACE;
   if (ws && !aligned16(ws)) return LCSA_ERR_INVALID_ARG;
   lcsa_attn_args x = *a;
   x.ckv = ws;
+  cudaStream_t st = (cudaStream_t)stream;
+  // dense attention works on whole tiles of 64 entries: those that no row sees are zeros
+  const long long nv = (a->q_pos0 + a->Tq - 1) / a->m, live = sparse || nv > a->Nc ? a->Nc : nv;
   if (a->Nc > 0) {
-    cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, a->Nc, ws, a->dtype,
-                                                    (cudaStream_t)stream);
+    cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, a->Nc, ws, a->dtype, st, live);
     if (err != cudaSuccess) return LCSA_ERR_CUDA;
   }
-  if (attn_fp4_supported(a))
-    return from_cuda(launch_attn_tc(&x, sparse, (char*)ws + fp4_expanded_bytes(a), (cudaStream_t)stream));
-  return from_cuda(launch_attn_generic(&x, sparse, (cudaStream_t)stream));
+  if (!attn_fp4_supported(a)) return from_cuda(launch_attn_generic(&x, sparse, st));
+  cudaError_t err = launch_attn_tc(&x, sparse, (char*)ws + fp4_expanded_bytes(a), st);
+  // rows whose window is not whole: its last tile there holds raw rows that they do not see
+  const long long part = (a->kv_pos0 > 0 ? a->kv_pos0 : 0) + a->W - 1 - a->q_pos0;
+  if (err == cudaSuccess && a->W > 0 && part > 0) err = launch_attn_fp4(a, sparse, e, st, (int)(part < a->Tq ? part : a->Tq));
+  return from_cuda(err);
 }
 
 lcsa_status lcsa_csa_sparse_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* ws, size_t ws_bytes,
