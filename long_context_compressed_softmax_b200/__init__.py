@@ -507,45 +507,53 @@ def empty_fp4_cache(B, rows, D=512, R=64, device="cuda"):
             torch.zeros((B, rows, R), dtype=torch.bfloat16, device=device))
 
 
+# Host time counts where a kernel takes microseconds: the checks below touch each tensor once, the stream's handle
+# is fetched without its object, and a device context is entered only when another device is current.
+_DT_CODE = {torch.float32: LCSA_FP32, torch.bfloat16: LCSA_BF16}
+
+
+def _code(t):
+    c = _DT_CODE.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return c
+
+
 def _fp4_cache(cache, B=None):
-    """The parts of a cache [B,rows,..], checked against each other -> (entries, B, rows, D, R)."""
+    """The parts of a cache [B,rows,..], checked against each other -> (entries, B, rows, D, R, device index)."""
     codes, scales, rope = cache
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or rope.dtype != torch.bfloat16:
         raise TypeError("an FP4 cache is (uint8 codes, uint8 scales, bfloat16 rope)")
-    _need_contig(codes, scales, rope)
-    sc, ss, sr = codes.shape, scales.shape, rope.shape
-    if len(sc) != 3 or len(ss) != 3 or len(sr) != 3 or not sc[0] == ss[0] == sr[0] or not sc[1] == ss[1] == sr[1]:
+    if not (codes.is_contiguous() and scales.is_contiguous() and rope.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    try:
+        b, rows, half = codes.shape
+        bs, rs, S = scales.shape
+        br, rr, R = rope.shape
+    except ValueError:
+        raise ValueError("FP4 cache parts must be [B, rows, ..]") from None
+    if bs != b or br != b or rs != rows or rr != rows:
         raise ValueError("FP4 cache parts must be [B, rows, ..] of the same B and rows")
-    R = sr[2]
-    D = 2 * sc[2] + R
-    if D <= R or R % 8 or (D - R) % 32 or ss[2] != ((D - R) // 32 + 15) // 16 * 16:
+    if half <= 0 or half % 16 or R % 8 or S != (half // 16 + 15) // 16 * 16:
         raise ValueError("FP4 cache parts do not fit together")
-    if B is not None and sc[0] != B:
+    if B is not None and b != B:
         raise ValueError("the FP4 cache holds another number of sequences")
-    _same_device(codes, scales, rope)
-    return Fp4Entries(codes.data_ptr(), scales.data_ptr(), rope.data_ptr()), sc[0], sc[1], D, R
+    dev = codes.get_device()
+    if dev < 0 or scales.get_device() != dev or rope.get_device() != dev:
+        raise ValueError("FP4 cache parts must be on one CUDA device")
+    return Fp4Entries(codes.data_ptr(), scales.data_ptr(), rope.data_ptr()), b, rows, 2 * half + R, R, dev
 
 
-def _same_device(*ts):
-    """The index of the CUDA device that all the tensors (None: no tensor) are on."""
-    dev = -1
+def _on_device(dev, *ts):
     for t in ts:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError("tensors must be on a CUDA device")
-        if dev >= 0 and d != dev:
-            raise ValueError("tensors must be on one device")
-        dev = d
-    return dev
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on one CUDA device")
 
 
 def _run(dev, fn, name, *args):
-    """fn(*args, stream) with device `dev` current, on its current stream.  (Host time counts where a kernel takes
-    microseconds: no context object when the device is current already, the stream's handle without its object.)"""
+    """fn(*args, stream) with device `dev` current, on its current stream."""
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -561,7 +569,8 @@ def quantize_entries_fp4(ckv, R=64, cache=None, row0=0):
     Without `cache`, ckv [..., D] gives new parts [..., (D-R)/2], [..., S] and
     [..., R].  With `cache` (parts [B,rows,..]), ckv [B,n,D] is written into
     rows row0 .. row0+n-1 of every sequence and the cache is returned."""
-    _need_contig(ckv)
+    if not ckv.is_contiguous():
+        raise ValueError("tensors must be contiguous")
     if cache is None:
         D = ckv.shape[-1]
         lead = ckv.shape[:-1]
@@ -572,11 +581,12 @@ def quantize_entries_fp4(ckv, R=64, cache=None, row0=0):
     if ckv.dim() != 3:
         raise ValueError("entries written into a cache are [B, n, D]")
     B, n, D = ckv.shape
-    e, _, rows, Dc, Rc = _fp4_cache(cache, B)
+    e, _, rows, Dc, Rc, dev = _fp4_cache(cache, B)
     if Dc != D or Rc != R:
         raise ValueError("the FP4 cache holds entries of another shape")
-    _run(_same_device(ckv, cache[0]), _lib.lcsa_quantize_entries_fp4, "quantize_entries_fp4", ckv.data_ptr(), B, n, D, R,
-         _dt(ckv), ctypes.byref(e), rows, int(row0))
+    _on_device(dev, ckv)
+    _run(dev, _lib.lcsa_quantize_entries_fp4, "quantize_entries_fp4", ckv.data_ptr(), B, n, D, R, _code(ckv), ctypes.byref(e),
+         rows, int(row0))
     return cache
 
 
@@ -584,22 +594,21 @@ def dequantize_entries_fp4(cache, idx=None, out_dtype=torch.bfloat16, out=None):
     """Entries read back from an FP4 cache (parts [B,rows,..]): all of them, or
     rows idx [B,n] int32 of each sequence (-1: a zero row) -> [B,n,D] out_dtype
     (BF16, or the same values in FP32)."""
-    e, B, rows, D, R = _fp4_cache(cache)
-    if idx is None:
-        n = rows
-    else:
-        _need_contig(idx)
+    e, B, n, D, _, dev = _fp4_cache(cache)
+    rows, R, idx_p = n, cache[2].shape[2], None
+    if idx is not None:
+        if not idx.is_contiguous():
+            raise ValueError("tensors must be contiguous")
         if idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != B:
             raise ValueError("idx must be int32 [B, n]")
-        n = idx.shape[1]
+        n, idx_p = idx.shape[1], idx.data_ptr()
     if out is None:
-        out = torch.empty((B, n, D), dtype=out_dtype, device=cache[0].device)
-    elif tuple(out.shape) != (B, n, D):
-        raise ValueError("out must be [B, n, D]")
-    else:
-        _need_contig(out)
-    _run(_same_device(cache[0], idx, out), _lib.lcsa_dequantize_entries_fp4, "dequantize_entries_fp4", ctypes.byref(e), B,
-         rows, D, R, None if idx is None else idx.data_ptr(), n, out.data_ptr(), _dt(out))
+        out = cache[0].new_empty((B, n, D), dtype=out_dtype)
+    elif tuple(out.shape) != (B, n, D) or not out.is_contiguous():
+        raise ValueError("out must be contiguous [B, n, D]")
+    _on_device(dev, idx, out)
+    _run(dev, _lib.lcsa_dequantize_entries_fp4, "dequantize_entries_fp4", ctypes.byref(e), B, rows, D, R, idx_p, n,
+         out.data_ptr(), _code(out))
     return out
 
 
@@ -607,7 +616,7 @@ def _attn_fp4(fn, name, sparse, q, cache, idx, kv, sink, q_pos0, kv_pos0, m, W, 
               out_dtype, return_lse, workspace, out):
     _need_contig(q, idx, kv, sink)
     B, Tq, H, D = q.shape
-    e, _, Nc, Dc, Rc = _fp4_cache(cache, B)
+    e, _, Nc, Dc, Rc, dev = _fp4_cache(cache, B)
     if Dc != D or Rc != R:
         raise ValueError("the FP4 cache holds entries of another shape")
     skv = kv.shape
@@ -624,17 +633,17 @@ def _attn_fp4(fn, name, sparse, q, cache, idx, kv, sink, q_pos0, kv_pos0, m, W, 
             raise ValueError("sink must be float32 [H]")
         sink_p = sink.data_ptr()
     if out is None:
-        out = torch.empty((B, Tq, H, D), dtype=out_dtype, device=q.device)
+        out = q.new_empty((B, Tq, H, D), dtype=out_dtype)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     else:
         _need_contig(out)
-    dev = _same_device(q, cache[0], idx, kv, sink, out, workspace)
+    _on_device(dev, q, idx, kv, sink, out, workspace)
     if return_lse:
         lse = torch.empty((B, Tq, H), dtype=torch.float32, device=q.device)
         lse_p = lse.data_ptr()
     a = AttnArgs(q.data_ptr(), None, idx_p, kv.data_ptr(), sink_p, B, Tq, H, D, R, Nc, k, skv[1], q_pos0, kv_pos0, m, W,
-                 softmax_scale, rope_base, _dt(q), out.data_ptr(), _dt(out), lse_p)
+                 softmax_scale, rope_base, _code(q), out.data_ptr(), _code(out), lse_p)
     pa = ctypes.byref(a)
     need = _lib.lcsa_attn_fp4_workspace(pa, sparse)
     if need > 0 and (workspace is None or workspace.numel() < need):
