@@ -494,9 +494,14 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
 /* Core attention (as lcsa_csa_sparse_attn / lcsa_hca_dense_attn) over entries
  * held in the FP4 cache `e` with cache_rows = a->Nc, instead of a->ckv (not
  * read; may be NULL).  Every other argument and result is that of the BF16
- * calls on the entries read back; R must meet the cache's constraints.  Rows
- * that a query does not attend to are not read: what they hold (Inf, NaN) does
- * not reach its output.  The workspace is lcsa_attn_fp4_workspace bytes. */
+ * calls on the entries read back; R must meet the cache's constraints.
+ * Entries and raw rows that no query row of the call attends to are not read:
+ * what they hold (Inf, NaN, nothing yet) does not reach an output.  Large calls
+ * (many query rows per entry) read the cache back once into the workspace; in
+ * those an Inf or NaN in an entry or raw row that some query rows attend to may
+ * also reach the outputs of its sequence's other rows, as in the BF16 calls.
+ * The workspace is lcsa_attn_fp4_workspace bytes (0 for decode); results do not
+ * depend on it. */
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse);
 lcsa_status lcsa_csa_sparse_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* workspace,
                                      size_t workspace_bytes, void* stream);

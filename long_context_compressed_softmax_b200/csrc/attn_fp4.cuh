@@ -10,8 +10,8 @@
 //   S = Q K^T   M = 64 heads, N = 64 keys, A (the queries) from tensor memory
 //   softmax     two threads a head, the reference moves when a logit exceeds it by 2^8
 //   O += P K    M = 64, N = 2 x 256 dims
-// The 16-bit K tile is made in shared memory from 368 bytes a key: twelve warps
-// expand codes and turn rotary dims while the tiles before are multiplied.
+// The 16-bit K tile is made in shared memory from 368 bytes a key: fourteen
+// warps expand codes and turn rotary dims while the tiles before are multiplied.
 // Forms with 128 keys or dims on the M side (full-rate MMAs) were measured
 // first and are slower here: with N = 64 both operands' shared-memory reads
 // take the whole bandwidth of shared memory, which the expansion needs too.
