@@ -532,6 +532,9 @@ static bool fp4_cache_ok(const lcsa_fp4_entries* c, int R) {
          aligned16(c->rope);
 }
 
+// B * rows rows of D values whose bytes do not fit into 64 bits.
+static bool fp4_rows_overflow(int B, int64_t rows, int D) { return rows > INT64_MAX / 8 / D / B; }
+
 size_t lcsa_fp4_scale_bytes(int D, int R) { return fp4_shape_ok(D, R) ? (size_t)fp4_scale_bytes(D, R) : 0; }
 
 lcsa_status lcsa_quantize_entries_fp4(const void* x, int B, int64_t n, int D, int R, lcsa_dtype dtype,
@@ -540,6 +543,7 @@ lcsa_status lcsa_quantize_entries_fp4(const void* x, int B, int64_t n, int D, in
     return LCSA_ERR_INVALID_ARG;
   if (row0 > cache_rows || n > cache_rows - row0) return LCSA_ERR_INVALID_ARG;
   if (B == 0 || n == 0) return LCSA_OK;
+  if (fp4_rows_overflow(B, cache_rows, D)) return LCSA_ERR_INVALID_ARG;
   if (!x || !aligned16(x) || !fp4_cache_ok(cache, R)) return LCSA_ERR_INVALID_ARG;
   if (!have_device()) return LCSA_ERR_CUDA;
   return from_cuda(launch_quantize_entries_fp4(x, B, n, D, R, dtype, cache, cache_rows, row0, (cudaStream_t)stream));
@@ -550,6 +554,7 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
   if (!valid_dtype(out_dtype) || !fp4_shape_ok(D, R) || B < 0 || n < 0 || cache_rows < 0) return LCSA_ERR_INVALID_ARG;
   if (!idx && n > cache_rows) return LCSA_ERR_INVALID_ARG;
   if (B == 0 || n == 0) return LCSA_OK;
+  if (fp4_rows_overflow(B, cache_rows, D) || fp4_rows_overflow(B, n, D)) return LCSA_ERR_INVALID_ARG;
   if (!out || !aligned16(out) || (reinterpret_cast<uintptr_t>(idx) & 3u)) return LCSA_ERR_INVALID_ARG;
   if (cache_rows > 0 && !fp4_cache_ok(cache, R)) return LCSA_ERR_INVALID_ARG;
   if (!have_device()) return LCSA_ERR_CUDA;

@@ -100,6 +100,15 @@ def test_dequantize_entries_fp4_checks_arguments(lcsa):
         assert call() == 4 and call(idx=0x5004, n=100) == 4
 
 
+def test_entries_beyond_64_bits_are_refused(lcsa):
+    L, bf, e = lcsa.lib, lcsa.LCSA_BF16, lcsa.Fp4Entries(0x1000, 0x2000, 0x3000)
+    huge = 2 ** 62
+    assert L.lcsa_quantize_entries_fp4(ctypes.c_void_p(0x4000), 4, huge, 512, 64, bf, ctypes.byref(e), huge, 0, None) == 1
+    assert L.lcsa_dequantize_entries_fp4(ctypes.byref(e), 4, huge, 512, 64, None, huge, ctypes.c_void_p(0x4000), bf, None) == 1
+    assert L.lcsa_dequantize_entries_fp4(ctypes.byref(e), 4, 8, 512, 64, ctypes.c_void_p(0x5000), huge, ctypes.c_void_p(0x4000), bf,
+                                         None) == 1
+
+
 def test_attn_fp4_checks_arguments(lcsa):
     L = lcsa.lib
     A = lambda **kw: lcsa.AttnArgs(**{**dict(q=0x10000, out=0x20000, kv=0x30000, idx=0x40000, B=1, Tq=1, H=64, D=512,

@@ -1,6 +1,10 @@
 """Attention over the FP4 entry cache where it can go wrong: extreme scales and logits, masked rows that hold Inf or
 NaN, holes in a selection, the read-back path of large calls, alignment, streams, captured graphs, and a decode step
 through the calls a server makes."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -305,6 +309,60 @@ def test_sizes_of_nothing_and_one(lcsa):
     assert (run(lcsa, none, empty, None, 5, 0, m, 0, sink=False) == 0).all()
     q0 = {**x, "q": x["q"][:, :0].contiguous()}
     assert run(lcsa, q0, cache, None, 5, 0, m, 1).shape == (B, 0, 64, 512)
+    assert lcsa.get_device_status() == 0
+
+
+FIRST_CALL = """
+import sys, torch
+import long_context_compressed_softmax_b200 as lcsa
+g = torch.Generator(device="cuda").manual_seed(5)
+B, Nc, m, W, p0 = int(sys.argv[1]), 3000, 4, 128, 12005
+t = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+q, kv = t(B, 1, 64, 512), t(B, W, 512)
+cache = lcsa.quantize_entries_fp4(t(B, Nc, 512), 64)
+idx = torch.arange(1024, dtype=torch.int32, device="cuda").expand(B, 1, -1).contiguous()
+call = lambda: lcsa.csa_sparse_attn_fp4(q, cache, idx, kv, None, p0, p0 - W + 1, m, W)
+if sys.argv[2] == "captured":
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = call()
+    graph.replay()
+else:
+    out = call()
+torch.cuda.synchronize()
+ref = lcsa.csa_sparse_attn(q, lcsa.dequantize_entries_fp4(cache), idx, kv, None, p0, p0 - W + 1, m, W)
+err = (out.float() - ref.float()).abs().max().item()
+assert err <= 2 * %r, err
+assert lcsa.get_device_status() == 0
+print("done")
+"""
+
+
+@pytest.mark.parametrize("how", ["eager", "captured"])
+def test_split_call_as_the_first_of_a_process(lcsa, how):
+    """A split call sets the kernel up by itself, in a capture too."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL % ATT_MAX, "1", how], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == ["done"]
+
+
+@pytest.mark.parametrize("sink", [False, True])
+def test_split_call_with_empty_splits(lcsa, sink):
+    """A selection whose keys all lie in one split, or of holes alone: parts without keys count for nothing."""
+    B, Nc, q_pos0, m, k = 1, 3000, 12005, 4, 1024
+    x, cache = inputs(lcsa, B, 1, Nc, 1, 47)
+    for live in (0, 1, 3):
+        idx = torch.full((B, 1, k), -1, dtype=torch.int32, device=DEV)
+        idx[..., k - live:] = torch.arange(live, dtype=torch.int32, device=DEV) * 7
+        out, lse = run(lcsa, x, cache, idx, q_pos0, q_pos0, m, 0, sink, return_lse=True)
+        ref, _ = oracle(x, cache, idx, q_pos0, q_pos0, m, 0, sink)
+        assert np.abs(np64(out).reshape(ref.shape) - ref).max() <= 3e-2     # of one key up to 5: 2 * 2^-9 * 5
+        if live == 0 and not sink:
+            assert (out == 0).all() and (lse == float("-inf")).all()
+        elif live == 0:
+            assert torch.allclose(lse[0, 0], x["sink"], rtol=1e-5, atol=1e-5)
     assert lcsa.get_device_status() == 0
 
 
