@@ -500,8 +500,9 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
  * (many query rows per entry) read the cache back once into the workspace; in
  * those an Inf or NaN in an entry or raw row that some query rows attend to may
  * also reach the outputs of its sequence's other rows, as in the BF16 calls.
- * The workspace is lcsa_attn_fp4_workspace bytes (0 for decode); results do not
- * depend on it. */
+ * The workspace is lcsa_attn_fp4_workspace bytes: 0 for BF16 with H = 64, D = 512,
+ * R = 64 while the rows are few, otherwise the entries read back (and more). Its
+ * contents before a call do not matter. */
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse);
 lcsa_status lcsa_csa_sparse_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* workspace,
                                      size_t workspace_bytes, void* stream);
