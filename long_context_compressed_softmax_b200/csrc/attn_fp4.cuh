@@ -1060,6 +1060,16 @@ static long long attn_fp4_tiles(const lcsa_attn_args* a, int sparse, int n_q) {
   return (n_c + kF4Keys - 1) / kF4Keys + (n_w + kF4Keys - 1) / kF4Keys;
 }
 
+// Rows of a sequence when the cache is read back for attn_tc.cuh.  Selected
+// entries are gathered: as many as the cache has.  A dense call reads whole
+// tiles: up to the last tile that a row sees, zeros behind its last entry.
+// That kernel takes these rows for the entries there are, so zeros follow only
+// where no row's position reaches past the cache's last entry.
+static long long attn_fp4_read_rows(const lcsa_attn_args* a, int sparse) {
+  const long long nv = (a->q_pos0 + a->Tq - 1) / a->m;
+  return sparse || nv > a->Nc ? a->Nc : (nv + kF4Keys - 1) / kF4Keys * kF4Keys;
+}
+
 // Whether to read the whole cache back once and attend over BF16 entries
 // (attn_tc.cuh) instead of expanding each tile where it is used.  Expanding
 // costs a tile some 0.25 us of an SM; reading back costs 0.33 ns an entry
@@ -1067,9 +1077,11 @@ static long long attn_fp4_tiles(const lcsa_attn_args* a, int sparse, int n_q) {
 // 2176 keys over 8192 entries 936 us here and 805 us read back, 2048 rows of
 // 1152 keys over 1024 entries 529 and 381 us; 64 sequences of one row, 8192
 // entries each, 139 us and 362 us.  That kernel multiplies whole tiles, masked
-// keys by a weight of zero, so a window has to end with its tile and be in kv.
+// keys by a weight of zero, so a window has to end with its tile and be in kv,
+// and the entries of a sequence with a tile (attn_fp4_read_rows).
 static bool attn_fp4_expands(const lcsa_attn_args* a, int sparse) {
   if (a->W % kF4Keys != 0 || (a->W > 0 && a->kv_pos0 + a->Tkv < a->q_pos0 + a->Tq)) return false;
+  if (!sparse && a->B > 1 && attn_fp4_read_rows(a, sparse) % kF4Keys != 0) return false;
   const double rows = (double)a->B * a->Tq;
   return rows * (double)attn_fp4_tiles(a, sparse, a->Tq) * (0.25 / 148.0) > (double)a->B * a->Nc * 0.33e-3 + 15.0;
 }

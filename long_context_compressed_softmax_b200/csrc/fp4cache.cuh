@@ -246,8 +246,8 @@ static cudaError_t launch_quantize_entries_fp4(const void* x, int B, long long n
 // Reading the cache back: row r of sequence b is entry idx[b, r] (entry r
 // without idx); -1 gives a zero row, any other index outside [0, cache_rows)
 // a zero row and LCSA_DEV_BAD_INDEX; so does, unreported, an entry from
-// live_rows on (entries that nobody is to see, whatever they hold).  Mostly the 2 D (4 D) bytes written per
-// row.  A block a lane, as above (131,072 selected rows of 512 values to BF16:
+// live_rows on (entries that nobody is to see, whatever they hold; without
+// idx, n may go past the cache).  Mostly the 2 D (4 D) bytes written per row.  A block a lane, as above (131,072 selected rows of 512 values to BF16:
 // 49.0 us with 8 values a lane, 43.2 us with 32).
 // ---------------------------------------------------------------------------
 template <typename To>
@@ -266,7 +266,7 @@ dequantize_entries_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* 
     const Fp4Row at = fp4_row(r, n);
     const long long e = idx ? (long long)__ldg(idx + r) : at.i;
     const bool there = e >= 0 && e < live_rows;
-    if ((e < -1 || e >= cache_rows) && ul == 0) report(LCSA_DEV_BAD_INDEX);
+    if (idx && (e < -1 || e >= cache_rows) && ul == 0) report(LCSA_DEV_BAD_INDEX);
     const long long src = at.b * cache_rows + e;
     for (int p = ul; p < pieces; p += 1 << lg) {
       To* to = out + r * D + 32 * p;

@@ -563,16 +563,23 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
                                                  out_dtype, (cudaStream_t)stream, cache_rows));
 }
 
-// The entries read back in the queries' dtype: for the CUDA-core kernel, and
-// for calls whose rows read each entry many times.
-static size_t fp4_expanded_bytes(const lcsa_attn_args* a) {
-  return align256((size_t)a->B * (size_t)a->Nc * (size_t)a->D * esize(a->dtype));
+// The call over entries read back in the queries' dtype: for the CUDA-core
+// kernel, and for calls whose rows read each entry many times.
+static lcsa_attn_args fp4_read_call(const lcsa_attn_args* a, int sparse) {
+  lcsa_attn_args x = *a;
+  if (attn_fp4_supported(a)) x.Nc = (int)attn_fp4_read_rows(a, sparse);
+  return x;
+}
+
+static size_t fp4_expanded_bytes(const lcsa_attn_args* x) {
+  return align256((size_t)x->B * (size_t)x->Nc * (size_t)x->D * esize(x->dtype));
 }
 
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse) {
   if (!a || a->B <= 0 || a->Tq <= 0 || a->Nc < 0 || a->D <= 0 || a->m <= 0 || !valid_dtype(a->dtype)) return 0;
-  if (attn_fp4_supported(a)) return attn_fp4_expands(a, sparse) ? fp4_expanded_bytes(a) + attn_tc_workspace(a, sparse) : 0;
-  return fp4_expanded_bytes(a);
+  if (attn_fp4_supported(a) && !attn_fp4_expands(a, sparse)) return 0;
+  const lcsa_attn_args x = fp4_read_call(a, sparse);
+  return fp4_expanded_bytes(&x) + (attn_fp4_supported(a) ? attn_tc_workspace(&x, sparse) : 0);
 }
 
 static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entries* e, int sparse, void* ws,
@@ -588,17 +595,17 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
   const size_t need = lcsa_attn_fp4_workspace(a, sparse);
   if (need > 0 && (!ws || ws_bytes < need)) return LCSA_ERR_WORKSPACE;
   if (ws && !aligned16(ws)) return LCSA_ERR_INVALID_ARG;
-  lcsa_attn_args x = *a;
+  lcsa_attn_args x = fp4_read_call(a, sparse);
   x.ckv = ws;
   cudaStream_t st = (cudaStream_t)stream;
   // dense attention works on whole tiles of 64 entries: those that no row sees are zeros
   const long long nv = (a->q_pos0 + a->Tq - 1) / a->m, live = sparse || nv > a->Nc ? a->Nc : nv;
-  if (a->Nc > 0) {
-    cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, a->Nc, ws, a->dtype, st, live);
+  if (x.Nc > 0) {
+    cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, x.Nc, ws, a->dtype, st, live);
     if (err != cudaSuccess) return LCSA_ERR_CUDA;
   }
   if (!attn_fp4_supported(a)) return from_cuda(launch_attn_generic(&x, sparse, st));
-  cudaError_t err = launch_attn_tc(&x, sparse, (char*)ws + fp4_expanded_bytes(a), st);
+  cudaError_t err = launch_attn_tc(&x, sparse, (char*)ws + fp4_expanded_bytes(&x), st);
   // rows whose window is not whole: its last tile there holds raw rows that they do not see
   const long long part = (a->kv_pos0 > 0 ? a->kv_pos0 : 0) + a->W - 1 - a->q_pos0;
   if (err == cudaSuccess && a->W > 0 && part > 0) err = launch_attn_fp4(a, sparse, e, st, (int)(part < a->Tq ? part : a->Tq));
