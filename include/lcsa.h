@@ -494,7 +494,9 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
 /* Core attention (as lcsa_csa_sparse_attn / lcsa_hca_dense_attn) over entries
  * held in the FP4 cache `e` with cache_rows = a->Nc, instead of a->ckv (not
  * read; may be NULL).  Every other argument and result is that of the BF16
- * calls on the entries read back; R must meet the cache's constraints.
+ * calls on the entries read back; R must meet the cache's constraints.  A row of
+ * a selection may have -1 (any negative number) anywhere, not at its end alone:
+ * such a slot is no key.
  * Entries and raw rows that no query row of the call attends to are not read:
  * what they hold (Inf, NaN, nothing yet) does not reach an output.  Large calls
  * (many query rows per entry) read the cache back once into the workspace; in

@@ -1049,6 +1049,53 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   cluster_sync_all();                                        // no CTA leaves while another reads its part
 }
 
+// Selections with their entries first and -1 behind them, for the kernels that
+// read a row up to its first -1.  A block a row, 2048 slots at a time, a warp
+// 256 of them with all its loads in flight (2048 rows of 2048 slots: 7.5 us;
+// a warp a row 14.6 us).
+__global__ void __launch_bounds__(256)
+fp4_pack_selection_kernel(const int32_t* __restrict__ idx, long long rows, int k, int32_t* __restrict__ out) {
+  __shared__ int s_live[2][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int turn = 0;
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int32_t* src = idx + r * k;
+    int32_t* dst = out + r * k;
+    int n = 0;                                               // entries so far
+    for (long long e0 = 0; e0 < k; e0 += 2048, turn ^= 1) {
+      const int left = (int)(k - e0) - 256 * warp - lane;           // slots from this lane's first on
+      int v[8], at[8], mine = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = left > 32 * u ? __ldg(src + (k - left) + 32 * u) : -1;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t live = __ballot_sync(0xffffffffu, v[u] >= 0);
+        at[u] = mine + __popc(live & ((1u << lane) - 1u));
+        mine += __popc(live);
+      }
+      if (lane == 0) s_live[turn][warp] = mine;
+      __syncthreads();                                       // the other turn's counts have been read by now
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w < warp) before += s_live[turn][w];
+        all += s_live[turn][w];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (v[u] >= 0) dst[n + before + at[u]] = v[u];
+      n += all;
+    }
+    for (long long e = n + (int)threadIdx.x; e < k; e += 256) dst[e] = -1;
+  }
+}
+static cudaError_t launch_fp4_pack_selection(const int32_t* idx, long long rows, int k, int32_t* out, cudaStream_t st) {
+  const long long most = 64LL * sm_count();
+  count_launch();
+  fp4_pack_selection_kernel<<<(unsigned)(rows < most ? rows : most), 256, 0, st>>>(idx, rows, k, out);
+  return cudaGetLastError();
+}
+
 static bool attn_fp4_supported(const lcsa_attn_args* a) {
   return a->dtype == LCSA_BF16 && a->H == 64 && a->D == 512 && a->R == 64;
 }

@@ -571,15 +571,19 @@ static lcsa_attn_args fp4_read_call(const lcsa_attn_args* a, int sparse) {
   return x;
 }
 
+// Its workspace: the entries, the selections without holes, what the kernel itself needs.
 static size_t fp4_expanded_bytes(const lcsa_attn_args* x) {
   return align256((size_t)x->B * (size_t)x->Nc * (size_t)x->D * esize(x->dtype));
+}
+static size_t fp4_packed_bytes(const lcsa_attn_args* x, int sparse) {
+  return sparse ? align256((size_t)x->B * (size_t)x->Tq * (size_t)x->k * sizeof(int32_t)) : 0;
 }
 
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse) {
   if (!a || a->B <= 0 || a->Tq <= 0 || a->Nc < 0 || a->D <= 0 || a->m <= 0 || !valid_dtype(a->dtype)) return 0;
   if (attn_fp4_supported(a) && !attn_fp4_expands(a, sparse)) return 0;
   const lcsa_attn_args x = fp4_read_call(a, sparse);
-  return fp4_expanded_bytes(&x) + (attn_fp4_supported(a) ? attn_tc_workspace(&x, sparse) : 0);
+  return fp4_expanded_bytes(&x) + fp4_packed_bytes(&x, sparse) + (attn_fp4_supported(a) ? attn_tc_workspace(&x, sparse) : 0);
 }
 
 static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entries* e, int sparse, void* ws,
@@ -604,8 +608,15 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
     cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, x.Nc, ws, a->dtype, st, live);
     if (err != cudaSuccess) return LCSA_ERR_CUDA;
   }
+  char* rest = (char*)ws + fp4_expanded_bytes(&x);
+  if (sparse) {
+    x.idx = (const int32_t*)rest;
+    cudaError_t err = launch_fp4_pack_selection(a->idx, (long long)a->B * a->Tq, a->k, (int32_t*)rest, st);
+    if (err != cudaSuccess) return LCSA_ERR_CUDA;
+    rest += fp4_packed_bytes(&x, sparse);
+  }
   if (!attn_fp4_supported(a)) return from_cuda(launch_attn_generic(&x, sparse, st));
-  cudaError_t err = launch_attn_tc(&x, sparse, (char*)ws + fp4_expanded_bytes(&x), st);
+  cudaError_t err = launch_attn_tc(&x, sparse, rest, st);
   // rows whose window is not whole: its last tile there holds raw rows that they do not see
   const long long part = (a->kv_pos0 > 0 ? a->kv_pos0 : 0) + a->W - 1 - a->q_pos0;
   if (err == cudaSuccess && a->W > 0 && part > 0) err = launch_attn_fp4(a, sparse, e, st, (int)(part < a->Tq ? part : a->Tq));

@@ -59,3 +59,66 @@ def test_large_dense_calls_keep_sequences_apart(lcsa, B, Nc):
     assert torch.equal(out[0], clean[0]) and torch.equal(lse2[0], lse[0])
     assert not torch.isfinite(out[1:]).any()           # those sequences see their NaN
     assert lcsa.get_device_status() == 0
+
+
+# ------------------------------------------------------------------ holes in a selection
+def holed(B, Tq, k, q_pos0, m, Nc, seed):
+    """A selection with holes, and the same entries without them (padded at the end)."""
+    idx = gen.make_topk_idx(B, Tq, k, [O.n_visible(q_pos0 + i, m, Nc) for i in range(Tq)], seed=seed, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    hole = torch.rand(idx.shape, generator=g, device=DEV) < 0.1
+    hole[..., k // 2] = True
+    hole[0, 0] = True                                  # nothing left
+    hole[0, 1, :-1] = True                             # only the last slot
+    hole[-1, 2, 0] = True
+    idx[hole] = -1
+    idx[0, 3, k // 3] = -5                             # any negative number is no key
+    tight = torch.full_like(idx, -1)
+    live = idx >= 0
+    place = live.cumsum(-1) - 1
+    b, i, s = live.nonzero(as_tuple=True)
+    tight[b, i, place[b, i, s]] = idx[b, i, s]
+    return idx, tight
+
+
+def check_holes(lcsa, x, cache, idx, tight, q_pos0, kv_pos0, m, W, R, rows, exact):
+    args = (x["kv"], x["sink"], q_pos0, kv_pos0, m, W, R)
+    out, lse = lcsa.csa_sparse_attn_fp4(x["q"], cache, idx, *args, return_lse=True)
+    assert lcsa.get_device_status() == 0
+    same, same_lse = lcsa.csa_sparse_attn_fp4(x["q"], cache, tight, *args, return_lse=True)
+    if exact:                                          # the same keys in the same order
+        assert torch.equal(out, same) and torch.equal(lse, same_lse)
+    else:                                              # each within ATT_MAX of the exact value, keys up to 5
+        assert (out - same).abs().max() <= 2 * 5 * ATT_MAX and (lse - same_lse).abs().max() <= 4e-3
+    d, q, kv, s = expand(cache), np64(x["q"]), np64(x["kv"]), np64(x["sink"])
+    for b, i in rows:
+        sel = idx[b, i].cpu().numpy()
+        ref, _ = O.attend_one(q[b, i], q_pos0 + i, sel[sel >= 0], d[b], m, kv[b], kv_pos0, W, s, R)
+        # (5: windows that are not whole leave means of few keys)
+        assert np.abs(np64(out[b, i]) - ref).max() <= (1 if exact else 5) * ATT_MAX
+
+
+@pytest.mark.parametrize("k", [600, 61])
+def test_holes_in_the_selections_of_a_large_call(lcsa, k):
+    B, Tq, q_pos0, m, W, Nc = 2, 1500 if k == 600 else 3000, 5000, 4, 128, 1475
+    x, cache = inputs(lcsa, B, Tq, Nc, W + Tq - 1, 62)
+    idx, tight = holed(B, Tq, k, q_pos0, m, Nc, 63)
+    rows = [(0, 0), (0, 1), (0, 2), (0, 3), (1, 2), (1, Tq - 1)]
+    assert lcsa.attn_fp4_workspace_bytes(x["q"], cache, idx, x["kv"], m, W, q_pos0=q_pos0, kv_pos0=q_pos0 - W + 1) > 0
+    check_holes(lcsa, x, cache, idx, tight, q_pos0, q_pos0 - W + 1, m, W, 64, rows, True)
+
+
+def test_holes_where_windows_are_not_whole(lcsa):
+    """A call whose first rows go to another kernel than the rest."""
+    B, Tq, q_pos0, m, W, Nc, k = 2, 1500, 40, 4, 128, 400, 300
+    x, cache = inputs(lcsa, B, Tq, Nc, q_pos0 + Tq, 64)
+    idx, tight = holed(B, Tq, k, q_pos0, m, Nc, 65)
+    check_holes(lcsa, x, cache, idx, tight, q_pos0, 0, m, W, 64, [(0, 0), (1, 50), (1, 86), (1, 87), (0, 1400)], False)
+
+
+@pytest.mark.parametrize("dtype,H,D,R", [("fp32", 4, 64, 32), ("bf16", 16, 512, 64), ("fp32", 64, 512, 64)])
+def test_holes_in_selections_of_other_shapes(lcsa, dtype, H, D, R):
+    B, Tq, Nc, q_pos0, m, W, k = 2, 5, 60, 230, 4, 64, 20
+    x, cache = inputs(lcsa, B, Tq, Nc, q_pos0 + Tq, 66, H=H, D=D, R=R, dtype=dtype)
+    idx, tight = holed(B, Tq, k, q_pos0, m, Nc, 67)
+    check_holes(lcsa, x, cache, idx, tight, q_pos0, 0, m, W, R, [(b, i) for b in range(B) for i in range(Tq)], True)
