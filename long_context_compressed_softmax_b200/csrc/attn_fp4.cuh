@@ -287,8 +287,8 @@ __device__ __forceinline__ void f4_merge(const F4Merge& m) {
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
           const int u = u0 + i * kF4Threads;
-          const float w = u < u1 && r0 + k < S ? wgt[r * 64 + (u >> 7)] : 0.f;
-          if (w != 0.f) {                                    // a split without keys left whatever was there
+          const float w = u < u1 && r0 + k < S ? wgt[r * 64 + (u >> 7)] : -1.f;
+          if (!(w < 0.f)) {                                  // a split without a tile left whatever was there
             o[i].x = fmaf(w, x[i][k].x, o[i].x);
             o[i].y = fmaf(w, x[i][k].y, o[i].y);
             o[i].z = fmaf(w, x[i][k].z, o[i].z);
@@ -727,7 +727,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         if (g.splits > 1) {
           if (half == 0) {
             s_ref[h] = -INFINITY;
-            s_l[h] = 0.f;
+            s_l[h] = -1.f;                                   // no tile, so no O
           }
         } else {
           const long long o0 = ((long long)q_row * 64 + 16 * (warp & 3)) * 512;
@@ -1032,13 +1032,14 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
     for (int r = 0; r < S; ++r) M = fmaxf(M, s_wgt[r * 64 + h]);
     float L = sk == -INFINITY ? 0.f : exp2f(sk - M);
     for (int r = 0; r < S; ++r) {
-      const float ref = s_wgt[r * 64 + h];
+      const float ref = s_wgt[r * 64 + h], sum = s_sum[r * 64 + h];
       const float f = ref == -INFINITY ? 0.f : exp2f(ref - M);
-      s_wgt[r * 64 + h] = f;
-      L += f == 0.f ? 0.f : f * s_sum[r * 64 + h];
+      s_wgt[r * 64 + h] = sum < 0.f ? -1.f : f;
+      if (!(sum < 0.f)) L += f * sum;                        // a NaN sum stays one beside far larger references
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    for (int r = 0; r < S; ++r) s_wgt[r * 64 + h] *= inv;
+    for (int r = 0; r < S; ++r)
+      if (!(s_wgt[r * 64 + h] < 0.f)) s_wgt[r * 64 + h] *= inv;
     if (split == 0 && g.lse) g.lse[q_row * 64 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
   __syncthreads();

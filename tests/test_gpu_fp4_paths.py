@@ -122,3 +122,31 @@ def test_holes_in_selections_of_other_shapes(lcsa, dtype, H, D, R):
     x, cache = inputs(lcsa, B, Tq, Nc, q_pos0 + Tq, 66, H=H, D=D, R=R, dtype=dtype)
     idx, tight = holed(B, Tq, k, q_pos0, m, Nc, 67)
     check_holes(lcsa, x, cache, idx, tight, q_pos0, 0, m, W, R, [(b, i) for b in range(B) for i in range(Tq)], True)
+
+
+# ------------------------------------------------------------------ NaN in one part of a long key list
+@pytest.mark.parametrize("B", [1, 140])
+@pytest.mark.parametrize("bad", [slice(40, 41), slice(0, 256)])
+@pytest.mark.parametrize("large", ["key", "sink"])
+def test_nan_reaches_the_output_beside_far_larger_logits(lcsa, B, bad, large):
+    """One key list over many CTAs (B = 1) or in one (B = 140): a NaN among keys whose weights vanish beside another
+    key's, or the sink's, is a NaN of the output."""
+    Nc, m, q_pos0, W = 3000, 4, 12005, 128
+    x, _ = inputs(lcsa, B, 1, Nc, W, 68)
+    base = torch.randn(512, generator=torch.Generator().manual_seed(3)).to(DEV)
+    base[448:] = 0                                     # rotation leaves the logits alone
+    x["q"] = (x["q"].float() * 0.1 + 4 * base).bfloat16()
+    x["ckv"] = (x["ckv"].float() * 0.1).bfloat16()
+    sink = x["sink"].clone()
+    if large == "key":
+        x["ckv"][:, 2900] = (4 * base).bfloat16()      # a logit of some 300
+    else:
+        sink += 300.0
+    cache = lcsa.quantize_entries_fp4(x["ckv"], 64)
+    call = lambda: lcsa.hca_dense_attn_fp4(x["q"], cache, x["kv"], sink, q_pos0, q_pos0 - W + 1, m, W, return_lse=True)
+    out, lse = call()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    cache[1][:, bad] = 255
+    out, lse = call()
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    assert lcsa.get_device_status() == 0
