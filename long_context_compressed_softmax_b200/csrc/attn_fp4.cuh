@@ -1126,9 +1126,13 @@ static long long attn_fp4_read_rows(const lcsa_attn_args* a, int sparse) {
 // 1152 keys over 1024 entries 529 and 381 us; 64 sequences of one row, 8192
 // entries each, 139 us and 362 us.  That kernel multiplies whole tiles, masked
 // keys by a weight of zero, so a window has to end with its tile and be in kv,
-// and the entries of a sequence with a tile (attn_fp4_read_rows).
+// and the entries of a sequence with a tile (attn_fp4_read_rows).  Beyond 2048
+// selected entries it splits every row, with 128 KB of partial outputs a split
+// to write and read (2048 rows of 2049 + 128 keys over 8192 entries 966 us here
+// and 1163 us read back, of 8192 + 128 over 16384 3351 and 3492 us).
 static bool attn_fp4_expands(const lcsa_attn_args* a, int sparse) {
   if (a->W % kF4Keys != 0 || (a->W > 0 && a->kv_pos0 + a->Tkv < a->q_pos0 + a->Tq)) return false;
+  if (sparse && a->k > kAtMaxIdx) return false;
   if (!sparse && a->B > 1 && attn_fp4_read_rows(a, sparse) % kF4Keys != 0) return false;
   const double rows = (double)a->B * a->Tq;
   return rows * (double)attn_fp4_tiles(a, sparse, a->Tq) * (0.25 / 148.0) > (double)a->B * a->Nc * 0.33e-3 + 15.0;

@@ -1,0 +1,31 @@
+"""Which way a call over the FP4 entry cache goes (seen by the workspace that it asks for) and what it refuses, without
+a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def lcsa():
+    from conftest import build_library
+    return build_library()
+
+
+def args(lcsa, **kw):
+    return lcsa.AttnArgs(**{**dict(q=0x10000, out=0x20000, kv=0x30000, idx=0x40000, B=1, Tq=2048, H=64, D=512, R=64, Nc=8192,
+                                   k=2048, Tkv=2048 + 127, m=4, W=128, q_pos0=30720, kv_pos0=30720 - 127,
+                                   dtype=lcsa.LCSA_BF16, out_dtype=lcsa.LCSA_BF16), **kw})
+
+
+def workspace(lcsa, sparse, **kw):
+    return lcsa.lib.lcsa_attn_fp4_workspace(ctypes.byref(args(lcsa, **kw)), sparse)
+
+
+def test_more_selected_entries_than_the_read_back_kernel_stages(lcsa):
+    """Beyond 2048 selected entries that kernel splits every row and writes 128 KB of partial outputs a split: a call of
+    the tile kernel needs no memory."""
+    assert workspace(lcsa, 1) > 0
+    for k in (2049, 4096, 8192):
+        assert workspace(lcsa, 1, k=k) == 0
+    assert workspace(lcsa, 0, m=128, Nc=1024, q_pos0=129024, kv_pos0=129024 - 127, k=0) > 0

@@ -150,3 +150,19 @@ def test_nan_reaches_the_output_beside_far_larger_logits(lcsa, B, bad, large):
     out, lse = call()
     assert torch.isnan(out).all() and torch.isnan(lse).all()
     assert lcsa.get_device_status() == 0
+
+
+# ------------------------------------------------------------------ long selections
+def test_many_rows_of_more_selected_entries_than_2048(lcsa):
+    """Calls that take no workspace whatever their rows."""
+    B, Tq, q_pos0, m, W, Nc, k = 1, 600, 16000, 4, 128, 4150, 2501
+    x, cache = inputs(lcsa, B, Tq, Nc, W + Tq - 1, 75)
+    idx = gen.make_topk_idx(B, Tq, k, [O.n_visible(q_pos0 + i, m, Nc) for i in range(Tq)], seed=76, device=DEV)
+    kv_pos0 = q_pos0 - W + 1
+    assert lcsa.attn_fp4_workspace_bytes(x["q"], cache, idx, x["kv"], m, W, q_pos0=q_pos0, kv_pos0=kv_pos0) == 0
+    out = lcsa.csa_sparse_attn_fp4(x["q"], cache, idx, x["kv"], x["sink"], q_pos0, kv_pos0, m, W)
+    rows = [(0, 0), (0, 311), (0, 599)]
+    want, _ = O.csa_sparse_attn(np64(x["q"]), expand(cache), idx.cpu().numpy(), np64(x["kv"]), q_pos0, kv_pos0, m, W,
+                                np64(x["sink"]), 64, rows=rows)
+    assert np.abs(np64(out)[[r[0] for r in rows], [r[1] for r in rows]] - want).max() <= ATT_MAX
+    assert lcsa.get_device_status() == 0
