@@ -1101,27 +1101,37 @@ static bool attn_fp4_supported(const lcsa_attn_args* a) {
   return a->dtype == LCSA_BF16 && a->H == 64 && a->D == 512 && a->R == 64;
 }
 
-// 64-key tiles of the longest key list of the first n_q rows.
-static long long attn_fp4_tiles(const lcsa_attn_args* a, int sparse, int n_q) {
+// Entries that the last of the first n_q rows sees.
+static long long attn_fp4_visible(const lcsa_attn_args* a, int n_q) {
   const long long nv = (a->q_pos0 + n_q - 1) / a->m;
-  const long long n_c = sparse ? a->k : (nv < a->Nc ? nv : a->Nc), n_w = a->W < a->Tkv ? a->W : a->Tkv;
+  return nv < a->Nc ? nv : a->Nc;
+}
+
+// 64-key tiles of the longest key list of the first n_q rows (a selection holds
+// no more entries than are visible).
+static long long attn_fp4_tiles(const lcsa_attn_args* a, int sparse, int n_q) {
+  const long long seen = attn_fp4_visible(a, n_q);
+  const long long n_c = sparse && a->k < seen ? a->k : seen, n_w = a->W < a->Tkv ? a->W : a->Tkv;
   return (n_c + kF4Keys - 1) / kF4Keys + (n_w + kF4Keys - 1) / kF4Keys;
 }
 
-// Rows of a sequence when the cache is read back for attn_tc.cuh.  Selected
-// entries are gathered: as many as the cache has.  A dense call reads whole
-// tiles: up to the last tile that a row sees, zeros behind its last entry.
-// That kernel takes these rows for the entries there are, so zeros follow only
-// where no row's position reaches past the cache's last entry.
+// Rows of a sequence when the cache is read back.  Selected entries are
+// gathered, and a selection is trusted: as many as the cache has.  A dense call
+// needs what its last row sees.  attn_tc.cuh reads whole tiles there: zeros
+// behind the last entry.  It takes these rows for the entries there are, so
+// zeros follow only where no row's position reaches past the cache's last entry.
 static long long attn_fp4_read_rows(const lcsa_attn_args* a, int sparse) {
   const long long nv = (a->q_pos0 + a->Tq - 1) / a->m;
-  return sparse || nv > a->Nc ? a->Nc : (nv + kF4Keys - 1) / kF4Keys * kF4Keys;
+  if (sparse || nv > a->Nc) return a->Nc;
+  return attn_fp4_supported(a) ? (nv + kF4Keys - 1) / kF4Keys * kF4Keys : nv;
 }
 
 // Whether to read the whole cache back once and attend over BF16 entries
 // (attn_tc.cuh) instead of expanding each tile where it is used.  Expanding
 // costs a tile some 0.25 us of an SM; reading back costs 0.33 ns an entry
-// (1.5 KB at 4.6 TB/s) and about 15 us of launches.  Measured: 2048 rows of
+// (1.5 KB at 4.6 TB/s) and about 15 us of launches.  A cache may be allocated
+// for a far longer context: what counts is the entries that are read back, and
+// the tiles that the rows have by now.  Measured: 2048 rows of
 // 2176 keys over 8192 entries 936 us here and 805 us read back, 2048 rows of
 // 1152 keys over 1024 entries 529 and 381 us; 64 sequences of one row, 8192
 // entries each, 139 us and 362 us.  That kernel multiplies whole tiles, masked
@@ -1135,7 +1145,8 @@ static bool attn_fp4_expands(const lcsa_attn_args* a, int sparse) {
   if (sparse && a->k > kAtMaxIdx) return false;
   if (!sparse && a->B > 1 && attn_fp4_read_rows(a, sparse) % kF4Keys != 0) return false;
   const double rows = (double)a->B * a->Tq;
-  return rows * (double)attn_fp4_tiles(a, sparse, a->Tq) * (0.25 / 148.0) > (double)a->B * a->Nc * 0.33e-3 + 15.0;
+  return rows * (double)attn_fp4_tiles(a, sparse, a->Tq) * (0.25 / 148.0) >
+         (double)a->B * attn_fp4_read_rows(a, sparse) * 0.33e-3 + 15.0;
 }
 
 // CTAs that run at the same time in clusters of `s`, on the current device

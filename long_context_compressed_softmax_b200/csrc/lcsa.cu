@@ -567,7 +567,7 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
 // kernel, and for calls whose rows read each entry many times.
 static lcsa_attn_args fp4_read_call(const lcsa_attn_args* a, int sparse) {
   lcsa_attn_args x = *a;
-  if (attn_fp4_supported(a)) x.Nc = (int)attn_fp4_read_rows(a, sparse);
+  x.Nc = (int)attn_fp4_read_rows(a, sparse);
   return x;
 }
 
@@ -581,9 +581,10 @@ static size_t fp4_packed_bytes(const lcsa_attn_args* x, int sparse) {
 
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse) {
   if (!a || a->B <= 0 || a->Tq <= 0 || a->Nc < 0 || a->D <= 0 || a->m <= 0 || !valid_dtype(a->dtype)) return 0;
-  if (attn_fp4_supported(a) && !attn_fp4_expands(a, sparse)) return 0;
+  if (!attn_fp4_supported(a)) return fp4_expanded_bytes(a) + fp4_packed_bytes(a, sparse);   // at any position
+  if (!attn_fp4_expands(a, sparse)) return 0;
   const lcsa_attn_args x = fp4_read_call(a, sparse);
-  return fp4_expanded_bytes(&x) + fp4_packed_bytes(&x, sparse) + (attn_fp4_supported(a) ? attn_tc_workspace(&x, sparse) : 0);
+  return fp4_expanded_bytes(&x) + fp4_packed_bytes(&x, sparse) + attn_tc_workspace(&x, sparse);
 }
 
 static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entries* e, int sparse, void* ws,
@@ -602,10 +603,9 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
   lcsa_attn_args x = fp4_read_call(a, sparse);
   x.ckv = ws;
   cudaStream_t st = (cudaStream_t)stream;
-  // dense attention works on whole tiles of 64 entries: those that no row sees are zeros
-  const long long nv = (a->q_pos0 + a->Tq - 1) / a->m, live = sparse || nv > a->Nc ? a->Nc : nv;
   if (x.Nc > 0) {
-    cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, x.Nc, ws, a->dtype, st, live);
+    cudaError_t err = launch_dequantize_entries_fp4(e, a->B, a->Nc, a->D, a->R, nullptr, x.Nc, ws, a->dtype, st,
+                                                    sparse ? a->Nc : attn_fp4_visible(a, a->Tq));
     if (err != cudaSuccess) return LCSA_ERR_CUDA;
   }
   char* rest = (char*)ws + fp4_expanded_bytes(&x);

@@ -29,3 +29,13 @@ def test_more_selected_entries_than_the_read_back_kernel_stages(lcsa):
     for k in (2049, 4096, 8192):
         assert workspace(lcsa, 1, k=k) == 0
     assert workspace(lcsa, 0, m=128, Nc=1024, q_pos0=129024, kv_pos0=129024 - 127, k=0) > 0
+
+
+def test_the_read_back_counts_what_is_visible(lcsa):
+    """The first rows of a prefill into a cache allocated for a long context."""
+    first = dict(q_pos0=0, kv_pos0=0, Tkv=2048)
+    assert workspace(lcsa, 1, **first, Nc=512) > 0
+    assert workspace(lcsa, 1, **first, Nc=262144) == 0         # 262,144 entries for 511 that can be selected
+    # dense calls read back no more than the last tile that a row sees
+    small, large = workspace(lcsa, 0, **first, Nc=512), workspace(lcsa, 0, **first, Nc=262144)
+    assert 512 * 1024 <= small == large

@@ -152,6 +152,34 @@ def test_nan_reaches_the_output_beside_far_larger_logits(lcsa, B, bad, large):
     assert lcsa.get_device_status() == 0
 
 
+# ------------------------------------------------------------------ capacity
+@pytest.mark.parametrize("sparse", [True, False])
+def test_a_cache_larger_than_its_entries(lcsa, sparse):
+    """The rows of a cache that is allocated for a longer context hold anything; many rows at its start."""
+    B, Tq, q_pos0, m, W, k = 2, 2048, 0, 4, 128, 512
+    n = (q_pos0 + Tq) // m
+    x, cache = inputs(lcsa, B, Tq, n, q_pos0 + Tq, 73)
+    idx = gen.make_topk_idx(B, Tq, k, [O.n_visible(q_pos0 + i, m, n) for i in range(Tq)], seed=74, device=DEV) if sparse else None
+    big = lcsa.empty_fp4_cache(B, 120000)
+    big[0].fill_(0x77)
+    big[1].fill_(255)
+    big[2].fill_(float("nan"))
+    for t, c in zip(big, cache):
+        t[:, :n] = c
+
+    def call(c):
+        if sparse:
+            return lcsa.csa_sparse_attn_fp4(x["q"], c, idx, x["kv"], x["sink"], q_pos0, 0, m, W)
+        return lcsa.hca_dense_attn_fp4(x["q"], c, x["kv"], x["sink"], q_pos0, 0, m, W)
+
+    want, got = call(cache), call(big)
+    if sparse:
+        assert (got - want).abs().max() <= 2 * 5 * ATT_MAX          # by another kernel
+    else:
+        assert torch.equal(got, want)
+    assert lcsa.get_device_status() == 0
+
+
 # ------------------------------------------------------------------ long selections
 def test_many_rows_of_more_selected_entries_than_2048(lcsa):
     """Calls that take no workspace whatever their rows."""
