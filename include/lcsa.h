@@ -497,14 +497,20 @@ lcsa_status lcsa_dequantize_entries_fp4(const lcsa_fp4_entries* cache, int B, in
  * calls on the entries read back; R must meet the cache's constraints.  A row of
  * a selection may have -1 (any negative number) anywhere, not at its end alone:
  * such a slot is no key.
- * Entries and raw rows that no query row of the call attends to are not read:
- * what they hold (Inf, NaN, nothing yet) does not reach an output.  Large calls
- * (many query rows per entry) read the cache back once into the workspace; in
- * those an Inf or NaN in an entry or raw row that some query rows attend to may
- * also reach the outputs of its sequence's other rows, as in the BF16 calls.
- * The workspace is lcsa_attn_fp4_workspace bytes: 0 for BF16 with H = 64, D = 512,
- * R = 64 while the rows are few, otherwise the entries read back (and more). Its
- * contents before a call do not matter. */
+ * What entries and raw rows that no query row of the call attends to hold (Inf,
+ * NaN, nothing yet) does not reach an output.  Large calls (many query rows per
+ * entry) read the cache back once into the workspace; in those an Inf or NaN in
+ * an entry or raw row that some query rows attend to may also reach the outputs
+ * of its sequence's other rows, as in the BF16 calls.
+ * lcsa_attn_fp4_workspace gives the bytes of workspace that this call can use:
+ *   - BF16 with H = 64, D = 512, R = 64: 0 while the rows are few, else the entries
+ *     read back and more.  The size depends on the call's positions (q_pos0,
+ *     kv_pos0) as on its shape, and may grow as a context does.  With a smaller
+ *     workspace, or none, the call expands entries tile by tile instead: the same
+ *     result to rounding, at about 1.2 to 1.5 times the time.
+ *   - other shapes: the entries in the queries' type and a copy of the selections,
+ *     whatever the positions.  A smaller workspace is LCSA_ERR_WORKSPACE.
+ * Its contents before a call do not matter. */
 size_t lcsa_attn_fp4_workspace(const lcsa_attn_args* a, int sparse);
 lcsa_status lcsa_csa_sparse_attn_fp4(const lcsa_attn_args* a, const lcsa_fp4_entries* e, void* workspace,
                                      size_t workspace_bytes, void* stream);

@@ -645,9 +645,10 @@ def _attn_fp4(fn, name, sparse, q, cache, idx, kv, sink, q_pos0, kv_pos0, m, W, 
     a = AttnArgs(q.data_ptr(), None, idx_p, kv.data_ptr(), sink_p, B, Tq, H, D, R, Nc, k, skv[1], q_pos0, kv_pos0, m, W,
                  softmax_scale, rope_base, _code(q), out.data_ptr(), _code(out), lse_p)
     pa = ctypes.byref(a)
-    need = _lib.lcsa_attn_fp4_workspace(pa, sparse)
-    if need > 0 and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:       # a caller's workspace is all that the call takes, however small
+        need = _lib.lcsa_attn_fp4_workspace(pa, sparse)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_p, ws_n = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _run(dev, fn, name, pa, ctypes.byref(e), ws_p, ws_n)
     return (out, lse) if return_lse else out
@@ -668,7 +669,10 @@ def hca_dense_attn_fp4(q, cache, kv, sink, q_pos0, kv_pos0, m=128, W=128, R=64, 
 
 
 def attn_fp4_workspace_bytes(q, cache, idx, kv, m, W, R=64, q_pos0=0, kv_pos0=0):
-    """Workspace of csa_sparse_attn_fp4 (idx given) or hca_dense_attn_fp4 (idx None)."""
+    """Workspace of csa_sparse_attn_fp4 (idx given) or hca_dense_attn_fp4 (idx None) at these positions, in bytes.
+
+    BF16 calls of 64 heads, D = 512 and R = 64 run with any workspace (a smaller one than this, or an empty one, means
+    expanding entries tile by tile); for other shapes the size holds at every position and a smaller one is refused."""
     a = AttnArgs(_p(q), None, _p(idx), _p(kv), None, *q.shape, R, cache[0].shape[1], idx.shape[2] if idx is not None else 0,
                  kv.shape[1], int(q_pos0), int(kv_pos0), m, W, 0.0, 0.0, _dt(q), _p(q), _dt(q), None)
     return int(_lib.lcsa_attn_fp4_workspace(ctypes.byref(a), 0 if idx is None else 1))

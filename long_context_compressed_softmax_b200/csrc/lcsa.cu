@@ -595,10 +595,12 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
   if ((long long)a->B * a->Tq == 0) return LCSA_OK;
   if (a->Nc > 0 && !fp4_cache_ok(e, a->R)) return LCSA_ERR_INVALID_ARG;
   if (!have_device()) return LCSA_ERR_CUDA;
-  if (attn_fp4_supported(a) && !attn_fp4_expands(a, sparse))
-    return from_cuda(launch_attn_fp4(a, sparse, e, (cudaStream_t)stream, a->Tq));
+  // the tile kernel needs no workspace: without the room to read the cache back it does a large call too
   const size_t need = lcsa_attn_fp4_workspace(a, sparse);
-  if (need > 0 && (!ws || ws_bytes < need)) return LCSA_ERR_WORKSPACE;
+  const bool room = need == 0 || (ws && ws_bytes >= need);
+  if (attn_fp4_supported(a) && !(attn_fp4_expands(a, sparse) && room))
+    return from_cuda(launch_attn_fp4(a, sparse, e, (cudaStream_t)stream, a->Tq));
+  if (!room) return LCSA_ERR_WORKSPACE;
   if (ws && !aligned16(ws)) return LCSA_ERR_INVALID_ARG;
   lcsa_attn_args x = fp4_read_call(a, sparse);
   x.ckv = ws;

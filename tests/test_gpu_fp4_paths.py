@@ -152,6 +152,48 @@ def test_nan_reaches_the_output_beside_far_larger_logits(lcsa, B, bad, large):
     assert lcsa.get_device_status() == 0
 
 
+# ------------------------------------------------------------------ workspaces
+@pytest.mark.parametrize("sparse", [True, False])
+def test_a_workspace_too_small_for_reading_back_is_left_alone(lcsa, sparse):
+    """Calls of the tile kernel's shape run without the room to read the cache back; nothing is allocated then."""
+    B, Tq, q_pos0, m, W, Nc, k = 2, 900, 5000, 4, 128, 1475, 600
+    x, cache = inputs(lcsa, B, Tq, Nc, W + Tq - 1, 69)
+    idx = gen.make_topk_idx(B, Tq, k, [O.n_visible(q_pos0 + i, m, Nc) for i in range(Tq)], seed=70, device=DEV) if sparse else None
+    kv_pos0 = q_pos0 - W + 1
+    need = lcsa.attn_fp4_workspace_bytes(x["q"], cache, idx, x["kv"], m, W, q_pos0=q_pos0, kv_pos0=kv_pos0)
+    assert need > 0
+    out = torch.zeros(B, Tq, 64, 512, device=DEV)
+
+    def call(**kw):
+        if sparse:
+            return lcsa.csa_sparse_attn_fp4(x["q"], cache, idx, x["kv"], x["sink"], q_pos0, kv_pos0, m, W, **kw)
+        return lcsa.hca_dense_attn_fp4(x["q"], cache, x["kv"], x["sink"], q_pos0, kv_pos0, m, W, **kw)
+
+    want = call()
+    for size in (need - 256, 0):
+        ws = torch.full((size,), 0x5A, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        held = torch.cuda.memory_allocated()
+        assert call(out=out.zero_(), workspace=ws) is out
+        assert torch.cuda.max_memory_allocated() == held
+        assert (ws == 0x5A).all()
+        assert (out - want).abs().max() <= 2 * ATT_MAX
+    assert lcsa.get_device_status() == 0
+
+
+def test_a_workspace_too_small_for_other_shapes_is_refused(lcsa):
+    B, Tq, Nc, q_pos0, m, W = 2, 5, 60, 230, 4, 64
+    x, cache = inputs(lcsa, B, Tq, Nc, q_pos0 + Tq, 71, H=4, D=64, R=32, dtype="fp32")
+    need = lcsa.attn_fp4_workspace_bytes(x["q"], cache, None, x["kv"], m, W, R=32, q_pos0=q_pos0)
+    assert need > 0
+    args = (x["q"], cache, x["kv"], x["sink"], q_pos0, 0, m, W, 32)
+    want = lcsa.hca_dense_attn_fp4(*args)
+    assert torch.equal(lcsa.hca_dense_attn_fp4(*args, workspace=torch.empty(need, dtype=torch.uint8, device=DEV)), want)
+    with pytest.raises(lcsa.LcsaError):
+        lcsa.hca_dense_attn_fp4(*args, workspace=torch.empty(need - 256, dtype=torch.uint8, device=DEV))
+
+
 # ------------------------------------------------------------------ capacity
 @pytest.mark.parametrize("sparse", [True, False])
 def test_a_cache_larger_than_its_entries(lcsa, sparse):
