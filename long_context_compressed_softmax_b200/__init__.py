@@ -614,7 +614,7 @@ def dequantize_entries_fp4(cache, idx=None, out_dtype=torch.bfloat16, out=None):
 
 def _attn_fp4(fn, name, sparse, q, cache, idx, kv, sink, q_pos0, kv_pos0, m, W, R, softmax_scale, rope_base,
               out_dtype, return_lse, workspace, out):
-    _need_contig(q, idx, kv, sink)
+    _need_contig(q, idx, kv, sink, workspace)
     B, Tq, H, D = q.shape
     e, _, Nc, Dc, Rc, dev = _fp4_cache(cache, B)
     if Dc != D or Rc != R:

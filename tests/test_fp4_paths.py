@@ -39,3 +39,15 @@ def test_the_read_back_counts_what_is_visible(lcsa):
     # dense calls read back no more than the last tile that a row sees
     small, large = workspace(lcsa, 0, **first, Nc=512), workspace(lcsa, 0, **first, Nc=262144)
     assert 512 * 1024 <= small == large
+
+
+def test_a_strided_workspace_is_refused(lcsa):
+    """Its size in elements is not the bytes behind its first one."""
+    c = (torch.zeros(1, 8, 224, dtype=torch.uint8), torch.zeros(1, 8, 16, dtype=torch.uint8),
+         torch.zeros(1, 8, 64, dtype=torch.bfloat16))
+    q, kv = torch.zeros(1, 1, 64, 512, dtype=torch.bfloat16), torch.zeros(1, 4, 512, dtype=torch.bfloat16)
+    for ws in (torch.zeros(64, dtype=torch.uint8)[::2], torch.zeros(1, dtype=torch.uint8).expand(4096)):
+        with pytest.raises(ValueError, match="contiguous"):
+            lcsa.hca_dense_attn_fp4(q, c, kv, None, 0, 0, workspace=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            lcsa.csa_sparse_attn_fp4(q, c, torch.zeros(1, 1, 1, dtype=torch.int32), kv, None, 0, 0, workspace=ws)
