@@ -533,7 +533,7 @@ static bool fp4_cache_ok(const lcsa_fp4_entries* c, int R) {
 }
 
 // B * rows rows of D values whose bytes do not fit into 64 bits.
-static bool fp4_rows_overflow(int B, int64_t rows, int D) { return rows > INT64_MAX / 8 / D / B; }
+static bool fp4_rows_overflow(int B, int64_t rows, int64_t D) { return rows > INT64_MAX / 8 / D / B; }
 
 size_t lcsa_fp4_scale_bytes(int D, int R) { return fp4_shape_ok(D, R) ? (size_t)fp4_scale_bytes(D, R) : 0; }
 
@@ -593,6 +593,9 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
   if (s != LCSA_OK) return s;
   if (!fp4_shape_ok(a->D, a->R)) return LCSA_ERR_INVALID_ARG;
   if ((long long)a->B * a->Tq == 0) return LCSA_OK;
+  if (fp4_rows_overflow(a->B, a->Nc, a->D) || fp4_rows_overflow(a->B, a->Tkv, a->D) ||
+      fp4_rows_overflow(a->B, a->Tq, (int64_t)a->H * a->D) || (sparse && fp4_rows_overflow(a->B, a->Tq, a->k)))
+    return LCSA_ERR_INVALID_ARG;
   if (a->Nc > 0 && !fp4_cache_ok(e, a->R)) return LCSA_ERR_INVALID_ARG;
   if (!have_device()) return LCSA_ERR_CUDA;
   // the tile kernel needs no workspace: without the room to read the cache back it does a large call too

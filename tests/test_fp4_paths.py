@@ -41,6 +41,19 @@ def test_the_read_back_counts_what_is_visible(lcsa):
     assert 512 * 1024 <= small == large
 
 
+def test_attention_over_entries_beyond_64_bits_is_refused(lcsa):
+    L, big = lcsa.lib, 2 ** 31 - 1
+    e = lcsa.Fp4Entries(0x50000, 0x60000, 0x70000)
+    for a in (args(lcsa, B=big, Nc=big, D=1504, R=64, Tq=1, H=1, Tkv=0, k=1),
+              args(lcsa, B=big, Tq=big, H=big, D=64, R=32, Nc=1, Tkv=0, k=1),
+              args(lcsa, B=big, Tq=1, H=1, D=1504, R=64, Nc=1, Tkv=big, k=1),
+              args(lcsa, B=big, Tq=big, H=1, D=64, R=32, Nc=1, Tkv=0, k=big)):
+        for f in (L.lcsa_csa_sparse_attn_fp4, L.lcsa_hca_dense_attn_fp4):
+            if f is L.lcsa_hca_dense_attn_fp4 and a.k == big:
+                continue
+            assert f(ctypes.byref(a), ctypes.byref(e), ctypes.c_void_p(0x100000), 1 << 62, None) == 1
+
+
 def test_a_strided_workspace_is_refused(lcsa):
     """Its size in elements is not the bytes behind its first one."""
     c = (torch.zeros(1, 8, 224, dtype=torch.uint8), torch.zeros(1, 8, 16, dtype=torch.uint8),
