@@ -194,6 +194,17 @@ def test_a_workspace_too_small_for_other_shapes_is_refused(lcsa):
         lcsa.hca_dense_attn_fp4(*args, workspace=torch.empty(need - 256, dtype=torch.uint8, device=DEV))
 
 
+# ------------------------------------------------------------------ arguments
+def test_positions_of_any_integer_type(lcsa):
+    """As in the calls over BF16 entries: numpy integers and tensors of one element are positions."""
+    B, Nc, q_pos0, m, W = 2, 100, 420, 4, 128
+    x, cache = inputs(lcsa, B, 1, Nc, W, 72)
+    want = lcsa.hca_dense_attn_fp4(x["q"], cache, x["kv"], x["sink"], q_pos0, q_pos0 - W + 1, m, W)
+    for t in (np.int64, np.int32, torch.tensor):
+        got = lcsa.hca_dense_attn_fp4(x["q"], cache, x["kv"], x["sink"], t(q_pos0), t(q_pos0 - W + 1), m, W)
+        assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ capacity
 @pytest.mark.parametrize("sparse", [True, False])
 def test_a_cache_larger_than_its_entries(lcsa, sparse):
@@ -235,4 +246,32 @@ def test_many_rows_of_more_selected_entries_than_2048(lcsa):
     want, _ = O.csa_sparse_attn(np64(x["q"]), expand(cache), idx.cpu().numpy(), np64(x["kv"]), q_pos0, kv_pos0, m, W,
                                 np64(x["sink"]), 64, rows=rows)
     assert np.abs(np64(out)[[r[0] for r in rows], [r[1] for r in rows]] - want).max() <= ATT_MAX
+    assert lcsa.get_device_status() == 0
+
+
+# ------------------------------------------------------------------ offsets
+def test_offsets_past_two_gigabytes(lcsa):
+    """Rows of a cache behind 2^31 bytes of codes and of rotary dims: written, read back and attended to as in a cache
+    of their own."""
+    B, Nc, m, W, k, D = 2, 9_000_000, 4, 128, 300, 512
+    q_pos0 = 4 * Nc + 2
+    g = torch.Generator(device=DEV).manual_seed(77)
+    new = torch.randn(B, 400, D, generator=g, device=DEV).bfloat16()
+    cache = lcsa.empty_fp4_cache(B, Nc)
+    lcsa.quantize_entries_fp4(new, 64, cache=cache, row0=Nc - 400)
+    own = lcsa.quantize_entries_fp4(new, 64)
+    for t, o in zip(cache, own):
+        assert torch.equal(t[:, Nc - 400:], o)
+        assert not t[1, :Nc - 400].any()
+    idx = torch.arange(Nc - 400, Nc, dtype=torch.int32, device=DEV).expand(B, -1).contiguous()
+    assert torch.equal(lcsa.dequantize_entries_fp4(cache, idx=idx), lcsa.dequantize_entries_fp4(own))
+    x = gen.make_attn_inputs(B, 1, 64, D, 1, W, "bf16", seed=78, device=DEV, unit_scale=True)
+    sel = idx[:, 400 - k:].reshape(B, 1, k).contiguous()
+    args = (x["sink"], q_pos0, q_pos0 - W + 1, m, W)
+    out = lcsa.csa_sparse_attn_fp4(x["q"], cache, sel, x["kv"], *args)
+    # positions count by their differences alone: the selected rows as entries 0 .. k-1 of a shorter sequence
+    e, t = expand(tuple(c[:, 400 - k:].contiguous() for c in own)), q_pos0 - (Nc - k) * m
+    for b in range(B):
+        want, _ = O.attend_one(np64(x["q"])[b, 0], t, np.arange(k), e[b], m, np64(x["kv"])[b], t - W + 1, W, np64(x["sink"]), 64)
+        assert np.abs(np64(out)[b, 0] - want).max() <= ATT_MAX
     assert lcsa.get_device_status() == 0
