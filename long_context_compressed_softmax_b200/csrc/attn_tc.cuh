@@ -1182,8 +1182,12 @@ inline std::atomic<int>& attn_gather_mode() {
 }
 
 // f8 != null: the entries come from the FP8 cache (a->ckv is not read).
+// first_row > 0: the rows before it of every sequence are left to another
+// kernel that runs after this one (items go from the last row down, so those
+// rows are the list's end; with key-range splits their outputs are written all
+// the same, from whatever the workspace holds).
 static cudaError_t launch_attn_tc(const lcsa_attn_args* a, int sparse, void* ws, cudaStream_t st,
-                                  const lcsa_fp8_entries* f8 = nullptr) {
+                                  const lcsa_fp8_entries* f8 = nullptr, int first_row = 0) {
   const AtPlan pl = attn_tc_plan(a, sparse);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   const double log_base = log(a->rope_base > 0.f ? (double)a->rope_base : 10000.0);
@@ -1248,7 +1252,7 @@ static cudaError_t launch_attn_tc(const lcsa_attn_args* a, int sparse, void* ws,
   g.splits = pl.splits;
   g.out_bf16 = a->out_dtype == LCSA_BF16;
   g.out_v8 = (reinterpret_cast<uintptr_t>(pl.splits > 1 ? (const void*)P.o_part : a->out) & 31u) == 0 ? 1 : 0;
-  g.n_items = (int)(rows * pl.splits);
+  g.n_items = (int)((long long)a->B * (a->Tq - first_row) * pl.splits);
   g.fp8 = f8 != nullptr;
   auto kern = g.fp8 ? attn_tc_kernel<true, false> : g4 ? attn_tc_kernel<false, true> : attn_tc_kernel<false, false>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);

@@ -621,10 +621,9 @@ static lcsa_status attn_fp4_common(const lcsa_attn_args* a, const lcsa_fp4_entri
     rest += fp4_packed_bytes(&x, sparse);
   }
   if (!attn_fp4_supported(a)) return from_cuda(launch_attn_generic(&x, sparse, st));
-  cudaError_t err = launch_attn_tc(&x, sparse, rest, st);
-  // rows whose window is not whole: its last tile there holds raw rows that they do not see
-  const long long part = (a->kv_pos0 > 0 ? a->kv_pos0 : 0) + a->W - 1 - a->q_pos0;
-  if (err == cudaSuccess && a->W > 0 && part > 0) err = launch_attn_fp4(a, sparse, e, st, (int)(part < a->Tq ? part : a->Tq));
+  const int part = attn_fp4_part_rows(a);
+  cudaError_t err = launch_attn_tc(&x, sparse, rest, st, nullptr, part);
+  if (err == cudaSuccess && part > 0) err = launch_attn_fp4(a, sparse, e, st, part);
   return from_cuda(err);
 }
 

@@ -41,6 +41,18 @@ def test_the_read_back_counts_what_is_visible(lcsa):
     assert 512 * 1024 <= small == large
 
 
+def test_the_read_back_counts_the_rows_that_it_serves(lcsa):
+    """Rows whose window begins before the raw rows do are the tile kernel's in any case."""
+    short = dict(B=32, Nc=50, k=512, q_pos0=0, kv_pos0=0)
+    assert workspace(lcsa, 1, **short, Tq=150, Tkv=150) == 0               # 32 prompts of 150 tokens: 23 rows of each are left
+    assert workspace(lcsa, 0, **short, Tq=150, Tkv=150) == 0
+    assert workspace(lcsa, 1, **{**short, "Nc": 1000}, Tq=1000, Tkv=1000) > 0
+    # the same rows with their windows in kv
+    whole = dict(B=32, Nc=1050, k=512, q_pos0=4000, kv_pos0=4000 - 127, Tq=150, Tkv=150 + 127)
+    assert workspace(lcsa, 1, **whole) > 0
+    assert workspace(lcsa, 1, **{**whole, "kv_pos0": 4200, "Tkv": 100}) == 0    # no row's window is whole
+
+
 def test_attention_over_entries_beyond_64_bits_is_refused(lcsa):
     L, big = lcsa.lib, 2 ** 31 - 1
     e = lcsa.Fp4Entries(0x50000, 0x60000, 0x70000)

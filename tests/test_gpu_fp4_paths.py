@@ -194,6 +194,40 @@ def test_a_workspace_too_small_for_other_shapes_is_refused(lcsa):
         lcsa.hca_dense_attn_fp4(*args, workspace=torch.empty(need - 256, dtype=torch.uint8, device=DEV))
 
 
+# ------------------------------------------------------------------ rows whose window is not whole
+@pytest.mark.parametrize("sparse", [True, False])
+@pytest.mark.parametrize("B,Tq,back", [(1, 200, 60), (3, 500, 0), (1, 700, 126)])
+def test_rows_whose_window_is_not_whole(lcsa, sparse, B, Tq, back):
+    """Their kernel's results, whatever the other rows' kernel (its keys split where the rows are few) finds in the
+    workspace."""
+    Nc, m, W, k = 8192 if Tq == 200 else 2048, 4, 128, 1024
+    q_pos0 = 4 * Nc - Tq
+    x, cache = inputs(lcsa, B, Tq, Nc, back + Tq, 79)
+    idx = gen.make_topk_idx(B, Tq, k, [O.n_visible(q_pos0 + i, m, Nc) for i in range(Tq)], seed=80, device=DEV) if sparse else None
+    kv_pos0 = q_pos0 - back
+    need = lcsa.attn_fp4_workspace_bytes(x["q"], cache, idx, x["kv"], m, W, q_pos0=q_pos0, kv_pos0=kv_pos0)
+    assert need > 0 or sparse and Tq == 200
+
+    def call(ws):
+        args = (x["kv"], x["sink"], q_pos0, kv_pos0, m, W)
+        kw = dict(return_lse=True, workspace=ws)
+        return lcsa.csa_sparse_attn_fp4(x["q"], cache, idx, *args, **kw) if sparse else lcsa.hca_dense_attn_fp4(x["q"], cache, *args, **kw)
+
+    want, want_lse = call(torch.empty(0, dtype=torch.uint8, device=DEV))
+    first = None
+    for fill in (0xFF, 0x3C):
+        out, lse = call(torch.full((need,), fill, dtype=torch.uint8, device=DEV))
+        assert (out - want).abs().max() <= 2 * ATT_MAX and (lse - want_lse).abs().max() <= 4e-3
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    rows = [(0, 0), (B - 1, 126 - back), (B - 1, 127 - back), (0, Tq - 1)]
+    sel = (idx.cpu().numpy(),) if sparse else ()
+    want, _ = (O.csa_sparse_attn if sparse else O.hca_dense_attn)(np64(x["q"]), expand(cache), *sel, np64(x["kv"]), q_pos0, kv_pos0,
+                                                                  m, W, np64(x["sink"]), 64, rows=rows)
+    assert np.abs(np64(out)[[r[0] for r in rows], [r[1] for r in rows]] - want).max() <= ATT_MAX
+    assert lcsa.get_device_status() == 0
+
+
 # ------------------------------------------------------------------ arguments
 def test_positions_of_any_integer_type(lcsa):
     """As in the calls over BF16 entries: numpy integers and tensors of one element are positions."""
