@@ -341,7 +341,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   uint64_t* stats_full = reinterpret_cast<uint64_t*>(smem + kF4BStats);     // [2] by item, softmax warps
   uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + kF4BQReady);       // transition warps
   uint64_t* s_done = reinterpret_cast<uint64_t*>(smem + kF4BSDone);         // MMA commit after an item's last S
-  uint64_t* drain = reinterpret_cast<uint64_t*>(smem + kF4BDrain);          // MMA commit of an abandoned CTA
+  uint64_t* drain = reinterpret_cast<uint64_t*>(smem + kF4BDrain);          // MMA commit after the last product
   __shared__ uint32_t s_tmem;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -876,10 +876,10 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         ++n;
         if (++st == kF4Stages) { st = 0; full_par ^= 1; }
       }
-      if (!ok) {                                             // products in flight end before tensor memory is freed
-        tc::mma_commit(drain);
-        tc::mbar_wait(drain, 0);
-      }
+      // products in flight end before tensor memory is freed, also where the
+      // roles that wait for them gave up
+      tc::mma_commit(drain);
+      tc::mbar_wait(drain, 0);
     }
   } else if (warp == kF4SeqWarp) {
     // ============================================================ sequencer
