@@ -592,7 +592,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       }
       l_run *= alpha;
       if (n >= 2 && !f4_wait<kF4BPvDone>(bar, ((n >> 1) - 1) & 1)) break;   // P's buffer has been read
-      // weights, rounded to BF16 for the product (2^-9 of a weight, averaged
+      // weights, rounded to BF16 for the product (2^-8 of a weight at most, averaged
       // over the keys); the sums keep the unrounded weights
       const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1142,8 +1142,8 @@ static int attn_fp4_part_rows(const lcsa_attn_args* a) {
 // (1.5 KB at 4.6 TB/s) and about 15 us of launches.  A cache may be allocated
 // for a far longer context: what counts is the entries that are read back, and
 // the tiles that the rows have by now.  Measured: 2048 rows of
-// 2176 keys over 8192 entries 936 us here and 805 us read back, 2048 rows of
-// 1152 keys over 1024 entries 529 and 381 us; 64 sequences of one row, 8192
+// 2176 keys over 8192 entries 938 us here and 811 us read back, 2048 rows of
+// 1152 keys over 1024 entries 535 and 377 us; 64 sequences of one row, 8192
 // entries each, 139 us and 362 us.  That kernel multiplies whole tiles, masked
 // keys by a weight of zero, so a window has to end with its tile and be in kv,
 // and the entries of a sequence with a tile (attn_fp4_read_rows).  Beyond 2048
