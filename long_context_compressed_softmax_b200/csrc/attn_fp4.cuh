@@ -69,10 +69,11 @@ static_assert(sizeof(F4Tile) % 16 == 0, "tile description");
 // shared-memory carve-up, offsets from the 1 KB aligned base
 constexpr uint32_t kF4OffP = kF4Stages * kF4KBytes;                    // two P tiles
 constexpr uint32_t kF4OffTab = kF4OffP + 2 * kF4PBytes;
-constexpr uint32_t kF4OffStats = kF4OffTab + kF4Ring * sizeof(F4Tile); // [2 items][64] (reference, sum)
-constexpr uint32_t kF4OffRef = kF4OffStats + 2 * 64 * 8;               // [64] of this split
+constexpr uint32_t kF4OffStats = kF4OffTab + kF4Ring * sizeof(F4Tile); // [2 items][64] (reference, sum, exact sum)
+constexpr uint32_t kF4OffRef = kF4OffStats + 2 * 64 * 16;              // [64] of this split
 constexpr uint32_t kF4OffL = kF4OffRef + 64 * 4;                       // [64]
-constexpr uint32_t kF4OffWgt = kF4OffL + 64 * 4;                       // [splits][64] merge weights
+constexpr uint32_t kF4OffE = kF4OffL + 64 * 4;                         // [64]
+constexpr uint32_t kF4OffWgt = kF4OffE + 64 * 4;                       // [splits][64] merge weights
 constexpr uint32_t kF4OffCs = kF4OffWgt + kF4MaxSplits * 64 * 4;       // [4 warps][2 items][32] (cos, sin)
 constexpr uint32_t kF4OffTurn = kF4OffCs + 4 * 64 * 8;                 // [32] turns per position
 constexpr uint32_t kF4OffBar = kF4OffTurn + 32 * 8;
@@ -323,9 +324,10 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   F4Tile* tab = reinterpret_cast<F4Tile*>(smem + kF4OffTab);
-  float2* s_stats = reinterpret_cast<float2*>(smem + kF4OffStats);
+  float4* s_stats = reinterpret_cast<float4*>(smem + kF4OffStats);
   float* s_ref = reinterpret_cast<float*>(smem + kF4OffRef);
   float* s_l = reinterpret_cast<float*>(smem + kF4OffL);
+  float* s_e = reinterpret_cast<float*>(smem + kF4OffE);
   float* s_wgt = reinterpret_cast<float*>(smem + kF4OffWgt);
   float2* s_cs = reinterpret_cast<float2*>(smem + kF4OffCs);
   unsigned long long* s_turn = reinterpret_cast<unsigned long long*>(smem + kF4OffTurn);
@@ -528,7 +530,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
     const int half = lane >> 4, h = 16 * (warp & 3) + (lane & 15);
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t prow = k_base + kF4OffP + h * 128;
-    float m_run = -INFINITY, l_run = 0.f;                    // l_run: this thread's half
+    float m_run = -INFINITY, l_run = 0.f, e_run = 0.f;       // the sums: of this thread's half
     bool ok = true;
     int n = 0, ni = 0;
     for (int ts = 0; ok; ++ts) {
@@ -569,7 +571,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       bool grow = false;
       if (first) {
         m_run = top;
-        l_run = 0.f;
+        l_run = e_run = 0.f;
       } else if (top > m_run + 8.f) {                        // otherwise weights stay below 2^8
         alpha = ex2_ftz(m_run - top);
         m_run = top;
@@ -591,11 +593,14 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         tc::tmem_wait_st();
       }
       l_run *= alpha;
+      e_run *= alpha;
       if (n >= 2 && !f4_wait<kF4BPvDone>(bar, ((n >> 1) - 1) & 1)) break;   // P's buffer has been read
-      // weights, rounded to BF16 for the product (2^-8 of a weight at most, averaged
-      // over the keys); the sums keep the unrounded weights
+      // Weights, rounded to BF16 for the product (2^-8 of a weight at most).
+      // Outputs are divided by the sum of the rounded weights, so what all of
+      // a query's weights have in common in their rounding cancels (few keys:
+      // half of the largest errors); the log-sum-exp takes the exact ones'.
       const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      f2x sum = pk2(0.f, 0.f), exact = sum;
 #pragma unroll 1
       for (int u = 0; u < 2; ++u) {
         logits(u);
@@ -606,9 +611,10 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
           for (int i = 0; i < 4; ++i) {
             const float p0 = ex2_ftz(fmaf(__uint_as_float(v[8 * c + 2 * i]), g.scale_log2, neg_m));
             const float p1 = ex2_ftz(fmaf(__uint_as_float(v[8 * c + 2 * i + 1]), g.scale_log2, neg_m));
-            sum[i] += p0 + p1;
             const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
             w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            exact = add2(exact, pk2(p0, p1));
+            sum = add2(sum, pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)));
           }
           f4_sts128(prow + sb * kF4PBytes + (((4 * half + 2 * u + c) ^ (h & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
         }
@@ -616,15 +622,17 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) f4_arrive<kF4BSFree>(bar);
-      l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 l2 = upk2(sum), e2 = upk2(exact);
+      l_run += l2.x + l2.y;
+      e_run += e2.x + e2.y;
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) f4_arrive<kF4BPFull>(bar);
       ++n;
       if (last) {
-        const float l = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
-        if (half == 0) s_stats[(ni & 1) * 64 + h] = make_float2(m_run, l);
+        const float l = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16), e = e_run + __shfl_xor_sync(0xffffffffu, e_run, 16);
+        if (half == 0) s_stats[(ni & 1) * 64 + h] = make_float4(m_run, l, e, 0.f);
         __syncwarp();
         if (lane == 0) f4_arrive<kF4BStats>(k_base + 8 * (ni & 1));
         ++ni;
@@ -644,25 +652,28 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       ok = f4_wait<kF4BStats>(k_base + 8 * (item & 1), (item >> 1) & 1) && ok;
       ok = f4_wait<kF4BPvDone>(k_base + 8 * (p_last & 1), (p_last >> 1) & 1) && ok;
       tc::tc_fence_after();
-      const float2 ml = s_stats[(item & 1) * 64 + h];        // (reference, sum)
+      const float4 ml = s_stats[(item & 1) * 64 + h];        // (reference, sum, exact sum)
       float f = 1.f;
       if (g.splits > 1) {
         if (half == 0) {
           // (a NaN sum stays one: its weights were taken against 0)
           s_ref[h] = ml.y == 0.f ? -INFINITY : ml.x == -INFINITY ? 0.f : ml.x;
           s_l[h] = ml.y;
+          s_e[h] = ml.z;
         }
       } else {
-        float M = ml.x, L = ml.y;
+        float M = ml.x, L = ml.y, E = ml.z;
         if (g.sink) {
           const float sk = g.sink[h] * 1.4426950408889634f;
           M = fmaxf(ml.x, sk);
           f = ml.x == -INFINITY ? (L == 0.f ? 0.f : 1.f) : exp2f(ml.x - M);
-          L = L * f + (sk == -INFINITY ? 0.f : exp2f(sk - M));
+          const float es = sk == -INFINITY ? 0.f : exp2f(sk - M);
+          L = L * f + es;
+          E = E * f + es;
         }
         // a row without keys and sink: zero output (a NaN sum stays one)
         f = L == 0.f ? 0.f : f / L;
-        if (half == 0 && g.lse) g.lse[(long long)p_row * 64 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        if (half == 0 && g.lse) g.lse[(long long)p_row * 64 + h] = E == 0.f ? -INFINITY : (M + log2f(E)) * 0.6931471805599453f;
       }
       const float2* c = cs + (item & 1) * 32;
       uint32_t buf[2][16];
@@ -727,7 +738,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         if (g.splits > 1) {
           if (half == 0) {
             s_ref[h] = -INFINITY;
-            s_l[h] = -1.f;                                   // no tile, so no O
+            s_l[h] = s_e[h] = -1.f;                          // no tile, so no O
           }
         } else {
           const long long o0 = ((long long)q_row * 64 + 16 * (warp & 3)) * 512;
@@ -1014,9 +1025,11 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   const long long q_row = qr.row, t = qr.t;
   // every split's references and sums, all loads in flight at once (P's space is free by now)
   float* s_sum = reinterpret_cast<float*>(smem + kF4OffP);
+  float* s_exact = s_sum + 64 * S;
   for (int i = threadIdx.x; i < 64 * S; i += kF4Threads) {
     s_wgt[i] = ld_cluster(cluster_addr(tc::smem_u32(s_ref + (i & 63)), i >> 6));
     s_sum[i] = ld_cluster(cluster_addr(tc::smem_u32(s_l + (i & 63)), i >> 6));
+    if (split == 0 && g.lse) s_exact[i] = ld_cluster(cluster_addr(tc::smem_u32(s_e + (i & 63)), i >> 6));
   }
   if (threadIdx.x >= kF4Threads - 32) {
     const int i = threadIdx.x & 31;
@@ -1030,17 +1043,20 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
     const float sk = g.sink ? g.sink[h] * 1.4426950408889634f : -INFINITY;
     float M = sk;
     for (int r = 0; r < S; ++r) M = fmaxf(M, s_wgt[r * 64 + h]);
-    float L = sk == -INFINITY ? 0.f : exp2f(sk - M);
+    float L = sk == -INFINITY ? 0.f : exp2f(sk - M), E = L;
     for (int r = 0; r < S; ++r) {
       const float ref = s_wgt[r * 64 + h], sum = s_sum[r * 64 + h];
       const float f = ref == -INFINITY ? 0.f : exp2f(ref - M);
       s_wgt[r * 64 + h] = sum < 0.f ? -1.f : f;
-      if (!(sum < 0.f)) L += f * sum;                        // a NaN sum stays one beside far larger references
+      if (!(sum < 0.f)) {                                    // a NaN sum stays one beside far larger references
+        L += f * sum;
+        if (split == 0 && g.lse) E += f * s_exact[r * 64 + h];
+      }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     for (int r = 0; r < S; ++r)
       if (!(s_wgt[r * 64 + h] < 0.f)) s_wgt[r * 64 + h] *= inv;
-    if (split == 0 && g.lse) g.lse[q_row * 64 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    if (split == 0 && g.lse) g.lse[q_row * 64 + h] = E == 0.f ? -INFINITY : (M + log2f(E)) * 0.6931471805599453f;
   }
   __syncthreads();
   const F4Merge m = {&g, smem, k_base, split, q_row};

@@ -309,3 +309,23 @@ def test_offsets_past_two_gigabytes(lcsa):
         want, _ = O.attend_one(np64(x["q"])[b, 0], t, np.arange(k), e[b], m, np64(x["kv"])[b], t - W + 1, W, np64(x["sink"]), 64)
         assert np.abs(np64(out)[b, 0] - want).max() <= ATT_MAX
     assert lcsa.get_device_status() == 0
+
+
+# ------------------------------------------------------------------ precision
+@pytest.mark.parametrize("B,Nc", [(1, 3000), (140, 40), (2, 1)])
+def test_weights_sum_to_one(lcsa, B, Nc):
+    """Dims in which all keys agree come back as they are, whatever the weights' rounding: FP32 sums of the rounded
+    weights, off by 2^-24 a step."""
+    m, W = 4, 128
+    q_pos0 = 4 * Nc + 3
+    x, _ = inputs(lcsa, B, 1, Nc, W, 81)
+    x["q"][..., 64:] = 0                               # logits from the first 64 dims, which differ
+    x["ckv"][..., 64:] = 1.5
+    x["kv"][..., 64:] = 1.5
+    x["ckv"][..., 448:] = x["kv"][..., 448:] = 0       # (dims that turn)
+    cache = lcsa.quantize_entries_fp4(x["ckv"], 64)
+    x["q"] = (x["q"].float() * 4).bfloat16()           # logits of standard deviation sqrt(64) * 4 / 22.6 = 1.4
+    out = lcsa.hca_dense_attn_fp4(x["q"], cache, x["kv"], None, q_pos0, q_pos0 - W + 1, m, W)
+    # sums of up to 64 products a tile and 49 tiles, two roundings each, in the numerator and the sum
+    assert (out[..., 64:448] - 1.5).abs().max() <= 1.5 * 2 * 113 * 2.0 ** -24 * 4
+    assert (out[..., 448:] == 0).all()
