@@ -4,9 +4,11 @@
 // window of raw BF16 rows, a per-head sink in the denominator, partial RoPE
 // and the -t rotation of the output.
 //
-//   out = R(-t) sum_j e^(l_j) k_j / (sum_j e^(l_j) + e^sink),  l_j = scale (R(t) q) . k_j
+//   out = R(-t) sum_j e^(l_j) R(p_j) k_j / (sum_j e^(l_j) + e^sink),  l_j = scale (R(t) q) . (R(p_j) k_j)
 //
-// with k_j rotated to its own position.  Tiles of 64 keys, three in flight:
+// A tile's keys are made for one query alone, so they are turned by p_j - t:
+// neither the query nor the output is rotated then, and the queries need no
+// rounding.  Tiles of 64 keys, three in flight:
 //   S = Q K^T   M = 64 heads, N = 64 keys, A (the queries) from tensor memory
 //   softmax     two threads a head, the reference moves when a logit exceeds it by 2^8
 //   O += P K    M = 64, N = 2 x 256 dims
@@ -58,10 +60,9 @@ struct F4Tile {
   int32_t first, last;       // of its query (and split)
   int32_t q_row;             // query row (b * Tq + i)
   uint32_t mask[2];          // keys that are there
-  int32_t pad[2];
+  int32_t pad[4];
   long long base;            // first row of the sequence in the cache or the raw buffer
-  long long pos0, step;      // position of row r: pos0 + r * step
-  long long t;               // position of the query
+  long long pos0, step;      // position of row r, from the query's: pos0 + r * step
 };
 constexpr int kF4Entries = 0, kF4Window = 1, kF4Empty = 2, kF4End = 3;
 static_assert(sizeof(F4Tile) % 16 == 0, "tile description");
@@ -74,9 +75,7 @@ constexpr uint32_t kF4OffRef = kF4OffStats + 2 * 64 * 16;              // [64] o
 constexpr uint32_t kF4OffL = kF4OffRef + 64 * 4;                       // [64]
 constexpr uint32_t kF4OffE = kF4OffL + 64 * 4;                         // [64]
 constexpr uint32_t kF4OffWgt = kF4OffE + 64 * 4;                       // [splits][64] merge weights
-constexpr uint32_t kF4OffCs = kF4OffWgt + kF4MaxSplits * 64 * 4;       // [4 warps][2 items][32] (cos, sin)
-constexpr uint32_t kF4OffTurn = kF4OffCs + 4 * 64 * 8;                 // [32] turns per position
-constexpr uint32_t kF4OffBar = kF4OffTurn + 32 * 8;
+constexpr uint32_t kF4OffBar = kF4OffWgt + kF4MaxSplits * 64 * 4;
 constexpr uint32_t kF4BTabFull = kF4OffBar, kF4BTabEmpty = kF4BTabFull + 8 * kF4Ring;
 constexpr uint32_t kF4BKFull = kF4BTabEmpty + 8 * kF4Ring, kF4BKEmpty = kF4BKFull + 8 * kF4Stages;
 constexpr uint32_t kF4BSFull = kF4BKEmpty + 8 * kF4Stages, kF4BSFree = kF4BSFull + 16, kF4BPFull = kF4BSFree + 16;
@@ -149,16 +148,13 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
   return v;
 }
 
-// (cos, sin) of an angle given as a 64-bit fraction of a turn.  Keys: the
-// MUFU's sine and cosine (2^-20 absolute) of an angle within half a turn,
-// far below the BF16 rounding of the rotated key.
-__device__ __forceinline__ void turn_cs_fast(unsigned long long ph, float* c, float* s) {
+// (cos, sin) of an angle given as a 64-bit fraction of a turn: the MUFU's sine
+// and cosine (2^-20 absolute) of an angle within half a turn, far below the
+// BF16 rounding of the rotated key.
+__device__ __forceinline__ void turn_cs(unsigned long long ph, float* c, float* s) {
   const float a = (float)(int)(ph >> 32) * 1.4629180792671596e-9f;   // 2 pi / 2^32
   *c = __cosf(a);
   *s = __sinf(a);
-}
-__device__ __forceinline__ void turn_cs(unsigned long long ph, float* c, float* s) {
-  sincospif((float)(int)(ph >> 32) * 4.656612873077393e-10f, s, c);   // 2 / 2^32 half turns
 }
 __device__ __forceinline__ uint32_t rotate_pair(uint32_t x, float c, float s) {
   const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
@@ -264,7 +260,6 @@ __device__ __forceinline__ void f4_merge(const F4Merge& m) {
   const F4Args& g = *m.g;
   const int S = g.splits, u1 = 8192 * (m.split + 1) / S;
   const float* wgt = reinterpret_cast<const float*>(m.smem + kF4OffWgt);
-  const float2* cs = reinterpret_cast<const float2*>(m.smem + kF4OffCs);
 #pragma unroll 1
   for (int u0 = 8192 * m.split / S + threadIdx.x; u0 < u1; u0 += kP * kF4Threads) {
     float4 o[kP];
@@ -303,11 +298,7 @@ __device__ __forceinline__ void f4_merge(const F4Merge& m) {
       const int u = u0 + i * kF4Threads;
       if (u >= u1) break;
       const int h = u >> 7, d = (u & 127) * 4;
-      float4 v = o[i];
-      if (d >= 448) {
-        const float2 e0 = cs[(d - 448) >> 1], e1 = cs[((d - 448) >> 1) + 1];
-        v = make_float4(v.x * e0.x + v.y * e0.y, v.y * e0.x - v.x * e0.y, v.z * e1.x + v.w * e1.y, v.w * e1.x - v.z * e1.y);
-      }
+      const float4 v = o[i];
       const long long at = (m.q_row * 64 + h) * 512 + d;
       if (g.out_bf16) {
         const float f[4] = {v.x, v.y, v.z, v.w};
@@ -329,8 +320,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   float* s_l = reinterpret_cast<float*>(smem + kF4OffL);
   float* s_e = reinterpret_cast<float*>(smem + kF4OffE);
   float* s_wgt = reinterpret_cast<float*>(smem + kF4OffWgt);
-  float2* s_cs = reinterpret_cast<float2*>(smem + kF4OffCs);
-  unsigned long long* s_turn = reinterpret_cast<unsigned long long*>(smem + kF4OffTurn);
   uint64_t* tab_full = reinterpret_cast<uint64_t*>(smem + kF4BTabFull);     // [kF4Ring] sequencer
   uint64_t* tab_empty = reinterpret_cast<uint64_t*>(smem + kF4BTabEmpty);   // [kF4Ring] every role's warps
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + kF4BKFull);        // [kF4Stages] expanding warps
@@ -369,7 +358,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
     tc::mbar_init(drain, 1);
     tc::fence_barrier_init();
   }
-  if (threadIdx.x < 32) s_turn[threadIdx.x] = g.turn[threadIdx.x];
   if (warp == kF4MmaWarp) { tc::tmem_alloc(&s_tmem, 512); tc::tmem_relinquish(); }
   tc::tc_fence_before();
   __syncthreads();
@@ -464,7 +452,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   } else if (xw < kF4Code + kF4Rot) {
     // ============================================================ rotary dims
     // Four 16-byte pieces a thread, always of the same four pairs, turned to
-    // the keys' positions.
+    // the keys' positions from the query's.
     const int tid = 32 * (xw - kF4Code) + lane;
     const uint32_t dst = k_base + 7 * kF4Region + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
     unsigned long long turn[4];
@@ -504,7 +492,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float co, si;
-          turn_cs_fast(pos * turn[i], &co, &si);
+          turn_cs(pos * turn[i], &co, &si);
           x[i] = rotate_pair(x[i], co, si);
         }
         rp[0] = rp[1];
@@ -645,7 +633,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
     // heads, two threads a head.
     const int half = lane >> 4, h = 16 * (warp & 3) + (lane & 15);
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    float2* cs = reinterpret_cast<float2*>(smem + kF4OffCs) + (warp & 3) * 64;   // [2 items][32] (cos, sin)
     bool ok = true;
     int n = 0, ni = 0, p_row = 0, p_last = 0;
     auto output = [&](int item) {                            // of the item before
@@ -675,10 +662,10 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         f = L == 0.f ? 0.f : f / L;
         if (half == 0 && g.lse) g.lse[(long long)p_row * 64 + h] = E == 0.f ? -INFINITY : (M + log2f(E)) * 0.6931471805599453f;
       }
-      const float2* c = cs + (item & 1) * 32;
       uint32_t buf[2][16];
       tc::tmem_ld_16x32bx2_x16<16>(t_lane + kF4TmO, buf[0]);
-#pragma unroll 2
+      // (by four: by two the compiler's code has a larger frame, and 64 x 8192 entries take 145 instead of 139 us)
+#pragma unroll 4
       for (int k = 0; k < 16; ++k) {                         // dims 32 k + 16 half ..
         uint32_t* v = buf[k & 1];
         tc::tmem_wait_ld_regs16(v);
@@ -698,15 +685,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-        if (k >= 14) {
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float2 e = c[(d0 - 448 + i) >> 1];         // rotated by -t
-            const float a0 = __uint_as_float(v[i]), a1 = __uint_as_float(v[i + 1]);
-            v[i] = __float_as_uint(a0 * e.x + a1 * e.y);
-            v[i + 1] = __float_as_uint(a1 * e.x - a0 * e.y);
-          }
-        }
         const long long o0 = ((long long)p_row * 64 + h) * 512 + d0;
         if (g.out_bf16) {
           uint32_t w[8];
@@ -730,7 +708,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
       const uint32_t d = f4_tile(k_base, ts);
       const int kind = (int)f4_lds32<offsetof(F4Tile, kind)>(d), first = (int)f4_lds32<offsetof(F4Tile, first)>(d),
                 last = (int)f4_lds32<offsetof(F4Tile, last)>(d), q_row = (int)f4_lds32<offsetof(F4Tile, q_row)>(d);
-      const unsigned long long t = f4_lds64<offsetof(F4Tile, t)>(d);
       __syncwarp();
       if (lane == 0) f4_arrive<kF4BTabEmpty>(k_base + 8 * (ts % kF4Ring));
       if (kind == kF4Empty) {
@@ -755,10 +732,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
         continue;
       }
       if (kind != kF4End && first) {
-        float c, s;
-        turn_cs(t * s_turn[lane], &c, &s);
-        cs[(ni & 1) * 32 + lane] = make_float2(c, s);
-        __syncwarp();
         // step k: dims 64 k + 32 half .. to 16 columns (two dims each), 16 further for the second half
         // (64 bytes a thread and step; 32-byte loads halve the requests, whose
         // number is what this takes)
@@ -772,15 +745,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (k + 2 < 8) ld_words<2>(q + 64 * (k + 2), x[(k + 2) % 3], wide);
-          uint32_t* r = x[k % 3];
-          if (k == 7) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = cs[(ni & 1) * 32 + 16 * half + i];
-              r[i] = rotate_pair(r[i], e.x, e.y);
-            }
-          }
-          tc::tmem_st_16x32bx2_x16<16>(t_lane + kF4TmQ + 32 * k, r);
+          tc::tmem_st_16x32bx2_x16<16>(t_lane + kF4TmQ + 32 * k, x[k % 3]);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -960,7 +925,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
           d.kind = kF4Empty;
           d.first = d.last = 0;
           d.q_row = (int)qr.row;
-          d.t = t;
         }
         publish();
         continue;
@@ -989,10 +953,9 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
           d.first = tile == t0;
           d.last = tile == t1 - 1;
           d.base = base;
-          d.pos0 = entries ? 0 : g.kv_pos0;
+          d.pos0 = (entries ? 0 : g.kv_pos0) - t;
           d.step = entries ? g.m : 1;
           d.q_row = (int)qr.row;
-          d.t = t;
         }
         publish();
         row[0] = next[0];
@@ -1021,8 +984,7 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
   // 512 outputs per CTA.
   cluster_sync_all();
   const int S = g.splits;
-  const F4Query qr = f4_query(g, blockIdx.x / S);
-  const long long q_row = qr.row, t = qr.t;
+  const long long q_row = f4_query(g, blockIdx.x / S).row;
   // every split's references and sums, all loads in flight at once (P's space is free by now)
   float* s_sum = reinterpret_cast<float*>(smem + kF4OffP);
   float* s_exact = s_sum + 64 * S;
@@ -1030,12 +992,6 @@ attn_fp4_kernel(const __grid_constant__ F4Args g) {
     s_wgt[i] = ld_cluster(cluster_addr(tc::smem_u32(s_ref + (i & 63)), i >> 6));
     s_sum[i] = ld_cluster(cluster_addr(tc::smem_u32(s_l + (i & 63)), i >> 6));
     if (split == 0 && g.lse) s_exact[i] = ld_cluster(cluster_addr(tc::smem_u32(s_e + (i & 63)), i >> 6));
-  }
-  if (threadIdx.x >= kF4Threads - 32) {
-    const int i = threadIdx.x & 31;
-    float c, s;
-    turn_cs((unsigned long long)t * s_turn[i], &c, &s);
-    s_cs[i] = make_float2(c, s);
   }
   __syncthreads();
   if (threadIdx.x < 64) {

@@ -329,3 +329,17 @@ def test_weights_sum_to_one(lcsa, B, Nc):
     # sums of up to 64 products a tile and 49 tiles, two roundings each, in the numerator and the sum
     assert (out[..., 64:448] - 1.5).abs().max() <= 1.5 * 2 * 113 * 2.0 ** -24 * 4
     assert (out[..., 448:] == 0).all()
+
+
+@pytest.mark.parametrize("t", [3, 1000, 1048575])
+def test_queries_are_not_rounded(lcsa, t):
+    """A key at the query's own position: its logit is the product of the two as given, at any position."""
+    B, W = 3, 1
+    x, cache = inputs(lcsa, B, 1, 1, 1, 82)
+    out, lse = lcsa.hca_dense_attn_fp4(x["q"], tuple(c[:, :0].contiguous() for c in cache), x["kv"], None, t, t, 128, W,
+                                       return_lse=True)
+    q, k = np64(x["q"])[:, 0], np64(x["kv"])[:, 0]
+    terms = np.abs(q * k[:, None]).sum(-1) * 512 ** -0.5
+    # 512 products summed in FP32 (2^-24 a step at most), the scale and the logarithm: a few roundings of the sum
+    assert (np.abs(np64(lse)[:, 0] - np.einsum("bhd,bd->bh", q, k) * 512 ** -0.5) <= terms * 520 * 2.0 ** -24).all()
+    assert torch.equal(out[:, 0], x["kv"].float().expand(-1, 64, -1))
